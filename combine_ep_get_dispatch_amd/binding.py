@@ -26,6 +26,10 @@ FP32 = 2
 SCALE_FP32 = 0
 SCALE_UE8M0 = 1
 
+# router scores (moedisp_score)
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+
 # host return codes
 OK = 0
 ERR_INVALID_ARG = -1
@@ -46,7 +50,9 @@ EXPORTS = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_dispatch_layout", 
            "ep_dispatch_notify", "ep_dispatch_scatter", "ep_dispatch_quant", "ep_dispatch_scatter_quant",
            "ep_dispatch_groups", "ep_group_permute", "ep_group_reduce", "ep_combine_groups",
            "ep_layout_dispatch_small", "ep_layout_dispatch_small_padded",
-           "ep_combine", "ep_combine_padded", "ep_check_status", "ep_status_string")
+           "ep_combine", "ep_combine_padded", "ep_check_status", "ep_status_string",
+           "ep_expert_gemm", "ep_expert_wgrad", "ep_swiglu_quant", "ep_swiglu_backward",
+           "ep_balance_workspace_bytes", "ep_balance_loss", "ep_balance_loss_backward")
 # tools (include/moedisp_tools.h): plan query and calibration probes, exported
 # by the same library
 CALIB_EXPORTS = ("ep_plan_query", "ep_probe_read", "ep_probe_copy", "ep_probe_fill")
@@ -69,6 +75,35 @@ class moedisp_shape(C.Structure):
 
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class moedisp_rows(C.Structure):
+    """Which rows belong to which expert (moedisp.h)."""
+    _fields_ = [("num_experts", C.c_int32), ("max_rows", C.c_int32), ("expert_stride", C.c_int32),
+                ("expert_capacity", C.c_int32), ("row_base", C.c_int32), ("expected_rows", C.c_int32)]
+
+    @classmethod
+    def contiguous(cls, num_experts, max_rows, expected_rows=0):
+        """Rows of ep_dispatch: row_bounds is its expert_offsets [E+1]."""
+        return cls(num_experts, max_rows, 0, 0, 0, expected_rows)
+
+    @classmethod
+    def padded(cls, num_experts, expert_capacity, expert_stride=None, row_base=0, expected_rows=0):
+        """Rows of ep_layout_dispatch_small_padded: row_bounds is its tokens_per_expert [E]."""
+        stride = expert_capacity if expert_stride is None else expert_stride
+        if not 0 <= num_experts * stride < 1 << 31:
+            raise MoeDispError("moedisp_rows", ERR_UNSUPPORTED, "E * expert_stride does not fit 31 bits")
+        return cls(num_experts, num_experts * stride, stride, expert_capacity, row_base, expected_rows)
+
+
+class moedisp_balance(C.Structure):
+    """A batch of sequences whose router balance is measured (moedisp.h)."""
+    _fields_ = [("num_seqs", C.c_int32), ("seq_len", C.c_int32), ("num_experts", C.c_int32), ("topk", C.c_int32),
+                ("score", C.c_int32), ("logits_dtype", C.c_int32), ("coef", C.c_float)]
+
+    @classmethod
+    def make(cls, num_seqs, seq_len, num_experts, topk, score=SCORE_SOFTMAX, logits_dtype=FP32, coef=1.0):
+        return cls(num_seqs, seq_len, num_experts, topk, score, logits_dtype, coef)
 
 
 class moedisp_launch_info(C.Structure):
@@ -170,6 +205,21 @@ def load(path: str = LIB_PATH):
     L.ep_check_status.restype = C.c_int
     L.ep_status_string.argtypes = [C.c_int]
     L.ep_status_string.restype = C.c_char_p
+    R, Bl, i32, sz = C.POINTER(moedisp_rows), C.POINTER(moedisp_balance), C.c_int32, C.c_size_t
+    L.ep_expert_gemm.argtypes = [R, i32, i32, i32, P, P, P, P, P, P, i32, P, sz, P]
+    L.ep_expert_gemm.restype = C.c_int
+    L.ep_expert_wgrad.argtypes = [R, i32, i32, i32, P, P, P, P, P, i32, i32, P, sz, P]
+    L.ep_expert_wgrad.restype = C.c_int
+    L.ep_swiglu_quant.argtypes = [R, i32, i32, P, P, P, P, P, sz, P]
+    L.ep_swiglu_quant.restype = C.c_int
+    L.ep_swiglu_backward.argtypes = [R, i32, i32, P, P, P, P, P, P, P, sz, P]
+    L.ep_swiglu_backward.restype = C.c_int
+    L.ep_balance_workspace_bytes.argtypes = [Bl]
+    L.ep_balance_workspace_bytes.restype = C.c_size_t
+    L.ep_balance_loss.argtypes = [Bl, P, P, P, P, P, P, sz, P]
+    L.ep_balance_loss.restype = C.c_int
+    L.ep_balance_loss_backward.argtypes = [Bl, P, P, P, P, P, P, P]
+    L.ep_balance_loss_backward.restype = C.c_int
     L.ep_plan_query.argtypes = [S, C.POINTER(moedisp_plan_info), C.c_size_t]
     L.ep_plan_query.restype = C.c_int
     L.ep_probe_read.argtypes = [P, C.c_size_t, P, P]
@@ -245,6 +295,20 @@ class _Args:
         for name, t in self.tensors:
             if t.device.type != "cuda":
                 self.fail(f"{name} is on {t.device}, expected a GPU tensor")
+
+    def on_device(self, stream):
+        """As done(); every tensor must lie on one GPU, the stream's if one is
+        given.  Returns the device and its stream (the device's current one
+        unless one is given), so that the call does not depend on which
+        device is current."""
+        self.done()
+        dev = self.tensors[0][1].device
+        for name, t in self.tensors:
+            if t.device != dev:
+                self.fail(f"{name} is on {t.device}, {self.tensors[0][0]} on {dev}")
+        if stream is not None and stream.device != dev:
+            self.fail(f"the stream is on {stream.device}, the tensors on {dev}")
+        return dev, _s(stream if stream is not None else torch.cuda.current_stream(dev))
 
 
 def _dims(shape: moedisp_shape):
@@ -592,6 +656,150 @@ def ep_combine_padded(shape, expert_stride, expert_out, recv_src_idx, recv_weigh
     _check(A.call, load().ep_combine_padded(
         C.byref(shape), int(expert_stride), _p(expert_out), _p(recv_src_idx), _p(recv_weights), _p(slot_to_row),
         _p(out), int(out_dtype), _p(ws), _nb(ws), _s(stream)))
+
+
+_E4M3 = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+
+
+def _need_rows(A, rows, row_bounds):
+    """max_rows, after checking the bounds' size."""
+    E = max(rows.num_experts, 0)
+    A.need("row_bounds", row_bounds, _INT32, 4 * (E + (0 if rows.expert_stride > 0 else 1)))
+    return max(rows.max_rows, 0)
+
+
+def _need_scales(A, name, t, fmt, count, optional=False):
+    A.need(name, t, _F32 if fmt == SCALE_FP32 else (torch.uint8,), (4 if fmt == SCALE_FP32 else 1) * count, optional)
+
+
+def _apart(A, name, *others):
+    """The written tensor `name` must not share memory with the others."""
+    by = dict(A.tensors)
+    if name not in by:
+        return
+    def span(t):
+        return t.data_ptr(), t.data_ptr() + _nb(t)
+    a0, a1 = span(by[name])
+    for o in others:
+        if o in by and by[o].device == by[name].device:
+            b0, b1 = span(by[o])
+            if a0 < b1 and b0 < a1:
+                A.fail(f"{name} overlaps {o}")
+
+
+def ep_expert_gemm(rows, n, k, scale_fmt, x, x_scales, w, w_scales, row_bounds, y, out_dtype, ws, stream=None):
+    A = _Args("ep_expert_gemm")
+    n, k, scale_fmt, out_dtype = int(n), int(k), int(scale_fmt), int(out_dtype)
+    R, E = _need_rows(A, rows, row_bounds), max(rows.num_experts, 0)
+    kb, nb = max(k, 0) // 128, (max(n, 0) + 127) // 128
+    A.need("x", x, _E4M3, R * max(k, 0))
+    _need_scales(A, "x_scales", x_scales, scale_fmt, R * kb)
+    A.need("w", w, _E4M3, E * max(n, 0) * max(k, 0))
+    _need_scales(A, "w_scales", w_scales, scale_fmt, E * nb * kb)
+    A.need("y", y, _out_dtypes(out_dtype), R * max(n, 0) * (4 if out_dtype == FP32 else 2))
+    _ws(A, ws)
+    _apart(A, "y", "x", "x_scales", "w", "w_scales", "row_bounds", "ws")
+    dev, st = A.on_device(stream)
+    with torch.cuda.device(dev):
+        _check(A.call, load().ep_expert_gemm(
+            C.byref(rows), n, k, scale_fmt, _p(x), _p(x_scales), _p(w), _p(w_scales), _p(row_bounds), _p(y),
+            out_dtype, _p(ws), _nb(ws), st))
+
+
+def ep_expert_wgrad(rows, n, k, scale_fmt, x, x_scales, dy, row_bounds, dw, out_dtype, accumulate, ws, stream=None):
+    A = _Args("ep_expert_wgrad")
+    n, k, scale_fmt, out_dtype = int(n), int(k), int(scale_fmt), int(out_dtype)
+    R, E = _need_rows(A, rows, row_bounds), max(rows.num_experts, 0)
+    A.need("x", x, _E4M3, R * max(k, 0))
+    _need_scales(A, "x_scales", x_scales, scale_fmt, R * (max(k, 0) // 128))
+    A.need("dy", dy, _ROWS_BF16, R * max(n, 0) * 2)
+    A.need("dw", dw, _out_dtypes(out_dtype), E * max(n, 0) * max(k, 0) * (4 if out_dtype == FP32 else 2))
+    _ws(A, ws)
+    _apart(A, "dw", "x", "x_scales", "dy", "row_bounds", "ws")
+    dev, st = A.on_device(stream)
+    with torch.cuda.device(dev):
+        _check(A.call, load().ep_expert_wgrad(
+            C.byref(rows), n, k, scale_fmt, _p(x), _p(x_scales), _p(dy), _p(row_bounds), _p(dw), out_dtype,
+            1 if accumulate else 0, _p(ws), _nb(ws), st))
+
+
+def ep_swiglu_quant(rows, inner, scale_fmt, gu, row_bounds, h, h_scales, ws, stream=None):
+    A = _Args("ep_swiglu_quant")
+    inner, scale_fmt = int(inner), int(scale_fmt)
+    R, I = _need_rows(A, rows, row_bounds), max(inner, 0)
+    A.need("gu", gu, _ROWS_BF16, R * I * 4)
+    A.need("h", h, _E4M3, R * I)
+    _need_scales(A, "h_scales", h_scales, scale_fmt, R * (I // 128))
+    _ws(A, ws)
+    _apart(A, "h", "gu", "h_scales", "row_bounds", "ws")
+    _apart(A, "h_scales", "gu", "row_bounds", "ws")
+    dev, st = A.on_device(stream)
+    with torch.cuda.device(dev):
+        _check(A.call, load().ep_swiglu_quant(
+            C.byref(rows), inner, scale_fmt, _p(gu), _p(row_bounds), _p(h), _p(h_scales), _p(ws), _nb(ws), st))
+
+
+def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, dgu_scales, ws, stream=None):
+    A = _Args("ep_swiglu_backward")
+    inner, scale_fmt = int(inner), int(scale_fmt)
+    R, I = _need_rows(A, rows, row_bounds), max(inner, 0)
+    A.need("gu", gu, _ROWS_BF16, R * I * 4)
+    A.need("dh", dh, _ROWS_BF16, R * I * 2)
+    A.need("dgu", dgu, _ROWS_BF16, R * I * 4, optional=True)
+    A.need("dgu_q", dgu_q, _E4M3, R * I * 2, optional=True)
+    _need_scales(A, "dgu_scales", dgu_scales, scale_fmt, R * (2 * I // 128), optional=True)
+    _ws(A, ws)
+    _apart(A, "dgu", "gu", "dh", "dgu_q", "dgu_scales", "row_bounds", "ws")
+    _apart(A, "dgu_q", "gu", "dh", "dgu_scales", "row_bounds", "ws")
+    _apart(A, "dgu_scales", "gu", "dh", "row_bounds", "ws")
+    dev, st = A.on_device(stream)
+    with torch.cuda.device(dev):
+        _check(A.call, load().ep_swiglu_backward(
+            C.byref(rows), inner, scale_fmt, _p(gu), _p(dh), _p(row_bounds), _p(dgu), _p(dgu_q), _p(dgu_scales),
+            _p(ws), _nb(ws), st))
+
+
+def ep_balance_workspace_bytes(balance) -> int:
+    return int(load().ep_balance_workspace_bytes(C.byref(balance)))
+
+
+def _need_balance(A, b, logits, topk_idx, tokens_per_expert, tokens_per_seq):
+    S, L, E, k = max(b.num_seqs, 0), max(b.seq_len, 0), max(b.num_experts, 0), max(b.topk, 0)
+    dt = (torch.bfloat16,) if b.logits_dtype == BF16 else _F32
+    nbytes = S * L * E * (2 if b.logits_dtype == BF16 else 4)
+    A.need("logits", logits, dt, nbytes)
+    A.need("topk_idx", topk_idx, _INT32, 4 * S * L * k)
+    A.need("tokens_per_expert", tokens_per_expert, _INT32, 4 * S * E)
+    A.need("tokens_per_seq", tokens_per_seq, _INT32, 4 * S)
+    return dt, nbytes
+
+
+def ep_balance_loss(balance, logits, topk_idx, loss, tokens_per_expert, tokens_per_seq, ws, stream=None):
+    A = _Args("ep_balance_loss")
+    _need_balance(A, balance, logits, topk_idx, tokens_per_expert, tokens_per_seq)
+    A.need("loss", loss, _F32, 4)
+    _ws(A, ws)
+    for o in ("loss", "tokens_per_expert", "tokens_per_seq", "ws"):
+        _apart(A, o, "logits", "topk_idx", *(q for q in ("loss", "tokens_per_expert", "tokens_per_seq", "ws") if q != o))
+    dev, st = A.on_device(stream)
+    with torch.cuda.device(dev):
+        _check(A.call, load().ep_balance_loss(
+            C.byref(balance), _p(logits), _p(topk_idx), _p(loss), _p(tokens_per_expert), _p(tokens_per_seq), _p(ws),
+            _nb(ws), st))
+
+
+def ep_balance_loss_backward(balance, logits, topk_idx, tokens_per_expert, tokens_per_seq, d_loss, d_logits,
+                             stream=None):
+    A = _Args("ep_balance_loss_backward")
+    dt, nbytes = _need_balance(A, balance, logits, topk_idx, tokens_per_expert, tokens_per_seq)
+    A.need("d_loss", d_loss, _F32, 4)
+    A.need("d_logits", d_logits, dt, nbytes)
+    _apart(A, "d_logits", "logits", "topk_idx", "tokens_per_expert", "tokens_per_seq", "d_loss")
+    dev, st = A.on_device(stream)
+    with torch.cuda.device(dev):
+        _check(A.call, load().ep_balance_loss_backward(
+            C.byref(balance), _p(logits), _p(topk_idx), _p(tokens_per_expert), _p(tokens_per_seq), _p(d_loss),
+            _p(d_logits), st))
 
 
 def ep_check_status(ws, stream=None) -> int:

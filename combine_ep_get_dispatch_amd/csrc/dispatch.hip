@@ -555,25 +555,6 @@ __global__ __launch_bounds__(kMaxDispatchThreads) void moedisp_scatter_pull_comp
 __device__ inline float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ inline float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Four E4M3 codes of (v0..v3), lowest byte first.
-__device__ inline uint32_t pack4_e4m3(float v0, float v1, float v2, float v3) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(v2, v3, w, true);
-    return (uint32_t)w;
-}
-
-__device__ inline float clamp448(float v) { return fminf(fmaxf(v, -448.0f), 448.0f); }
-
-// UE8M0 exponent of a block (amax finite, >= 0).
-__device__ inline int ue8m0_exponent(float amax) {
-    if (amax == 0.0f) return 0;
-    int ex;
-    const float m = frexpf(amax, &ex);  // amax = m * 2^ex, m in [0.5, 1)
-    // 448 * 2^(ex-9) = 0.875 * 2^ex covers amax iff m <= 0.875
-    const int s = ex - 9 + (m > 0.875f ? 1 : 0);
-    return min(127, max(-127, s));
-}
-
 // FMT: MOEDISP_SCALE_FP32 or MOEDISP_SCALE_UE8M0.
 template <int FMT>
 __global__ __launch_bounds__(kMaxDispatchThreads) void moedisp_scatter_quant(DispatchArgs a) {

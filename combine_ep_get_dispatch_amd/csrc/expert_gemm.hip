@@ -1,0 +1,281 @@
+// Product of the experts' rows with their weights, both E4M3 with a scale per
+// block of 128 channels:
+//     y[r][n] = sum_b sx[r][b] * sw[e][n/128][b] * (x[r][128b..] . w[e][n][128b..])
+#include "experts_common.h"
+
+namespace moedisp {
+namespace {
+
+constexpr int kBlk = kScaleBlock;
+
+// Loads of `SIZE` bytes per lane straight into LDS at `lds` + lane * max(4, SIZE).
+template <int SIZE>
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t rs, char* lds, int voff, int soff) {
+    auto* to = (__attribute__((address_space(3))) void*)lds;
+    if constexpr (SIZE == 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, voff, soff, 0, 0);
+    else if constexpr (SIZE == 4)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 4, voff, soff, 0, 0);
+    else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 1, voff, soff, 0, 0);
+}
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7FFFFFFF, kRawBufferWord3);
+}
+
+constexpr long long kLdsBytes = 160 * 1024;  // of a CU
+
+template <int N>
+__device__ inline void wait_loads_and_sync() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 32 bytes of an operand row: 16-byte chunks 2q and 2q+1 of the row's 8,
+// stored at chunk ^ swizzle.
+__device__ inline v8i read_frag(const char* row, int sw, int q) {
+    const v4i lo = *reinterpret_cast<const v4i*>(row + (((2 * q) ^ sw) << 4));
+    const v4i hi = *reinterpret_cast<const v4i*>(row + (((2 * q + 1) ^ sw) << 4));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+// 8 E4M3 codes (dwords 2j, 2j+1 of a fragment) as bf16, exactly.
+__device__ inline v8bf widen(const v8i& f, int j) {
+    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * j], 1.0f, false);
+    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * j], 1.0f, true);
+    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * j + 1], 1.0f, false);
+    const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * j + 1], 1.0f, true);
+    return v8bf{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// A scale's value from its stored bits (a UE8M0 byte in a dword).
+template <int FMT>
+__device__ inline float scale_value(int bits) {
+    return FMT == MOEDISP_SCALE_FP32 ? __int_as_float(bits) : ue8m0_value((uint32_t)bits);
+}
+
+__device__ inline int swizzle_w(int row) { return ((row >> 1) & 1) | (((row >> 3) & 3) << 1); }
+__device__ inline int swizzle_x(int row) { return (row >> 1) & 7; }
+
+template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
+struct Tile {
+    static constexpr int kWaves = WM * WN;
+    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kM = BM / WM;          // rows of a wave
+    static constexpr int kN = BN / WN;          // columns of a wave
+    static constexpr int kMT = kM / 16;
+    static constexpr int kNT = kN / 16;
+    static constexpr int kWLoads = BN / 8 / kWaves;  // 1 KiB loads of a wave and stage
+    static constexpr int kXLoads = (BM / 8 + kWaves - 1) / kWaves;
+    static constexpr int kLoads = kWLoads + kXLoads + 1;
+    static constexpr int kXBytes = kXLoads * kWaves * 1024;
+    static constexpr int kStage = BN * kBlk + kXBytes + kWaves * 256;
+    static constexpr int kSwBlocks = BN >= kBlk ? BN / kBlk : 1;
+    static_assert(kM <= 64 && kM % 16 == 0 && kN % 32 == 0 && kN <= kBlk && BN % (8 * kWaves) == 0, "tile shape");
+    static size_t lds(int kb) { return (size_t)STAGES * kStage + (size_t)kSwBlocks * kb * 4; }
+};
+
+template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
+__global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmArgs a) {
+    using T = Tile<BM, BN, WM, WN, STAGES, FMT, F32>;
+    constexpr int SB = FMT == MOEDISP_SCALE_FP32 ? 4 : 1;
+    extern __shared__ char lds[];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    int incl, own;
+    const int tiles = expert_tiles<BM>(a.r, &incl, &own);
+    if (tiles < 0) {
+        if (blockIdx.x == 0 && tid == 0) atomicOr(&a.hdr->status, (uint32_t)MOEDISP_DEV_BAD_LAYOUT);
+        return;
+    }
+    // XCD x (consecutive workgroups go round the XCDs) takes the x-th run of
+    // the tiles, its workgroups every (gridDim / 8)-th of them
+    const int total = tiles * a.nt;
+    const int per = (total + kXcds - 1) / kXcds;
+    const int end = min(total, ((int)(blockIdx.x % kXcds) + 1) * per);
+    for (int item = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds; item < end; item += gridDim.x / kXcds) {
+    const ExpertSpan s = expert_of_tile<BM>(a.r, item / a.nt, incl, own);
+    // an expert's tiles: groups of kGroup row tiles, columns, row tiles
+    constexpr int kGroup = 8;
+    const int mt = (s.count + BM - 1) / BM;
+    const int j0 = item - s.tiles_before * a.nt;
+    const int g = j0 / (kGroup * a.nt);
+    const int gm = min(kGroup, mt - g * kGroup);
+    const int jr = j0 - g * kGroup * a.nt;
+    const int ni = jr / gm;
+    const int n0 = ni * BN;
+    const int m0 = (g * kGroup + jr - ni * gm) * BM;
+    const int rows = min(BM, s.count - m0);
+    const int cols = min(BN, a.n - n0);
+
+    const size_t row0 = (size_t)s.first + m0;
+    const uint8_t* wp = a.w + ((size_t)s.e * a.n + n0) * a.k;
+    const uint8_t* xp = a.x + row0 * a.k;
+    const auto wrs = buffer_of(wp), xrs = buffer_of(xp);
+    const auto srs = buffer_of((const char*)a.x_scales + row0 * a.kb * SB);
+
+    int woff[T::kWLoads], xoff[T::kXLoads];
+#pragma unroll
+    for (int i = 0; i < T::kWLoads; ++i) {
+        const int row = (wave * T::kWLoads + i) * 8 + (lane >> 3);
+        woff[i] = min(row, cols - 1) * a.k + (((lane & 7) ^ swizzle_w(row)) << 4);
+    }
+#pragma unroll
+    for (int i = 0; i < T::kXLoads; ++i) {
+        const int row = (wave * T::kXLoads + i) * 8 + (lane >> 3);
+        xoff[i] = min(row, rows - 1) * a.k + (((lane & 7) ^ swizzle_x(row)) << 4);
+    }
+    const int wm = wave % WM, wn = wave / WM;
+    const int soff = min(wm * T::kM + lane, rows - 1) * a.kb * SB;
+
+    auto issue = [&](int kb, int buf) {
+        char* st = lds + buf * T::kStage;
+#pragma unroll
+        for (int i = 0; i < T::kWLoads; ++i)
+            load_to_lds<16>(wrs, st + (wave * T::kWLoads + i) * 1024, woff[i], kb * kBlk);
+#pragma unroll
+        for (int i = 0; i < T::kXLoads; ++i)
+            load_to_lds<16>(xrs, st + BN * kBlk + (wave * T::kXLoads + i) * 1024, xoff[i], kb * kBlk);
+        load_to_lds<SB>(srs, st + BN * kBlk + T::kXBytes + wave * 256, soff, kb * SB);
+    };
+
+    __syncthreads();  // the last tile's reads of LDS are done
+    // the weights' scales of the tile, all of k
+    int* sw = reinterpret_cast<int*>(lds + STAGES * T::kStage);
+    for (int i = tid; i < T::kSwBlocks * a.kb; i += T::kThreads) {
+        const int b = i / a.kb;
+        const size_t at = ((size_t)s.e * a.nb + min(n0 / kBlk + b, a.nb - 1)) * a.kb + (i - b * a.kb);
+        sw[i] = FMT == MOEDISP_SCALE_FP32 ? reinterpret_cast<const int*>(a.w_scales)[at]
+                                          : (int)reinterpret_cast<const uint8_t*>(a.w_scales)[at];
+    }
+    const int* swp = sw + (T::kSwBlocks > 1 ? (wn * T::kN / kBlk) * a.kb : 0);
+
+    v4f acc[T::kNT][T::kMT];
+#pragma unroll
+    for (int i = 0; i < T::kNT; ++i)
+#pragma unroll
+        for (int j = 0; j < T::kMT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+    for (int p = 0; p < STAGES - 1; ++p)
+        if (p < a.kb) issue(p, p);
+
+    const int q = lane >> 4, c = lane & 15;
+    const int wrow = wn * T::kN + (c >> 2) * 8 + (c & 3);
+    const int xrow = wm * T::kM + c;
+    const int wsw = swizzle_w(wrow), xsw = swizzle_x(xrow);
+    int buf = 0, nbuf = STAGES - 1;
+    for (int kb = 0; kb < a.kb; ++kb) {
+        if (kb + STAGES - 1 < a.kb) {
+            wait_loads_and_sync<(STAGES - 2) * T::kLoads>();
+            issue(kb + STAGES - 1, nbuf);
+        } else {
+            wait_loads_and_sync<0>();
+        }
+        const char* st = lds + buf * T::kStage;
+        const char* wt = st + wrow * kBlk;
+        const char* xt = st + BN * kBlk + xrow * kBlk;
+        const int* sx = reinterpret_cast<const int*>(st + BN * kBlk + T::kXBytes + wave * 256);
+        const int swv = swp[kb];
+        v8i b[T::kMT];
+        int sxv[T::kMT];
+#pragma unroll
+        for (int j = 0; j < T::kMT; ++j) {
+            b[j] = read_frag(xt + j * 16 * kBlk, xsw, q);
+            sxv[j] = sx[j * 16 + c];
+        }
+        // scale of the block's partial sums; the power-of-two scales of bf16
+        // results go into the matrix instruction
+        constexpr bool PROMOTE = FMT == MOEDISP_SCALE_FP32 || F32;
+        float f[T::kMT];
+        if (PROMOTE) {
+#pragma unroll
+            for (int j = 0; j < T::kMT; ++j) f[j] = scale_value<FMT>(sxv[j]) * scale_value<FMT>(swv);
+        }
+#pragma unroll
+        for (int i = 0; i < T::kNT; ++i) {
+            const v8i w = read_frag(wt + ((i >> 1) * 32 + (i & 1) * 4) * kBlk, wsw, q);
+#pragma unroll
+            for (int j = 0; j < T::kMT; ++j) {
+                if (PROMOTE) {
+                    v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (F32) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w, h), widen(b[j], h), p, 0, 0, 0);
+                    } else {
+                        p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, b[j], p, 0, 0, 0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], f[j], acc[i][j][v]);
+                } else {
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, b[j], acc[i][j], 0, 0, 0, swv, 0,
+                                                                                 sxv[j]);
+                }
+            }
+        }
+        buf = buf + 1 == STAGES ? 0 : buf + 1;
+        nbuf = nbuf + 1 == STAGES ? 0 : nbuf + 1;
+    }
+
+#pragma unroll
+    for (int j = 0; j < T::kMT; ++j) {
+        const int m = wm * T::kM + j * 16 + c;
+        if (m >= rows) continue;
+#pragma unroll
+        for (int t = 0; t < T::kNT / 2; ++t) {
+            const int n = wn * T::kN + t * 32 + q * 8;
+            if (n >= cols) continue;
+            const size_t at = (row0 + m) * a.n + n0 + n;
+            const v4f lo = acc[2 * t][j], hi = acc[2 * t + 1][j];
+            if (F32) {
+                v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at);
+                o[0] = lo;
+                o[1] = hi;
+            } else {
+                const v4u v = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                               pack_bf16x2(hi[2], hi[3])};
+                *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.y) + at) = v;
+            }
+        }
+    }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
+hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
+    using T = Tile<BM, BN, WM, WN, STAGES, FMT, F32>;
+    a.nt = (a.n + BN - 1) / BN;
+    const long long tiles = (long long)a.r.max_rows / BM + a.r.E;  // at least the tiles of any bounds
+    if (tiles * a.nt > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    const size_t lds = T::lds(a.kb);
+    long long blocks = (tiles * a.nt + kXcds - 1) / kXcds * kXcds;
+    const long long resident = 256 * (kLdsBytes / (long long)lds);
+    if (blocks > resident) blocks = resident;
+    hipLaunchKernelGGL((moedisp_expert_gemm<BM, BN, WM, WN, STAGES, FMT, F32>), dim3((unsigned)blocks),
+                       dim3(T::kThreads), lds, stream, a);
+    return hipGetLastError();
+}
+
+template <int FMT, bool F32>
+hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
+    return launch_tile<64, 128, 1, 4, 2, FMT, F32>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_expert_gemm(const ExpertGemmArgs& a, int mean_rows, int scale_fmt, bool f32_out,
+                              hipStream_t stream) {
+    if (scale_fmt == MOEDISP_SCALE_UE8M0)
+        return f32_out ? launch_variant<MOEDISP_SCALE_UE8M0, true>(a, mean_rows, stream)
+                       : launch_variant<MOEDISP_SCALE_UE8M0, false>(a, mean_rows, stream);
+    return f32_out ? launch_variant<MOEDISP_SCALE_FP32, true>(a, mean_rows, stream)
+                   : launch_variant<MOEDISP_SCALE_FP32, false>(a, mean_rows, stream);
+}
+
+}  // namespace moedisp

@@ -354,4 +354,23 @@ static __device__ inline uint32_t pull_sort(const DispatchArgs& a, int b, int32_
     return err;
 }
 
+// Four E4M3 codes of (v0..v3), lowest byte first.
+static __device__ inline uint32_t pack4_e4m3(float v0, float v1, float v2, float v3) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(v2, v3, w, true);
+    return (uint32_t)w;
+}
+
+static __device__ inline float clamp448(float v) { return fminf(fmaxf(v, -448.0f), 448.0f); }
+
+// UE8M0 exponent of a block (amax finite, >= 0).
+static __device__ inline int ue8m0_exponent(float amax) {
+    if (amax == 0.0f) return 0;
+    int ex;
+    const float m = frexpf(amax, &ex);  // amax = m * 2^ex, m in [0.5, 1)
+    // 448 * 2^(ex-9) = 0.875 * 2^ex covers amax iff m <= 0.875
+    const int s = ex - 9 + (m > 0.875f ? 1 : 0);
+    return min(127, max(-127, s));
+}
+
 }  // namespace moedisp

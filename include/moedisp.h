@@ -362,6 +362,149 @@ int ep_combine_padded(const moedisp_shape* shape, int32_t expert_stride, const v
                       const int32_t* recv_src_idx, const float* recv_weights, const int32_t* slot_to_row,
                       void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
 
+/* Experts' products and their parts, between dispatch and combine.
+ *
+ * moedisp_rows says which rows of a row buffer belong to which expert:
+ *   contiguous  expert_stride 0: expert e owns rows [row_bounds[e],
+ *               row_bounds[e+1]); row_bounds is ep_dispatch's expert_offsets,
+ *               int32 [E+1].  max_rows is the buffers' capacity (T*k).
+ *   padded      expert_stride > 0: expert e owns min(row_bounds[e],
+ *               expert_capacity) rows from e*expert_stride + row_base on;
+ *               row_bounds is the tokens_per_expert of
+ *               ep_layout_dispatch_small_padded, int32 [E].  max_rows is
+ *               E*expert_stride.
+ * Only those rows are read and written: rows behind the last expert's, and
+ * padded rows that no slot took, stay as they were.  Row bounds that are
+ * negative, decreasing or beyond max_rows set BAD_LAYOUT in `ws` and the call
+ * writes nothing (padded: a negative count does).  An expert may have no row.
+ * expected_rows only steers speed: the rows an expert usually gets, or 0 for
+ * max_rows / E (contiguous) or expert_capacity (padded).  Set it for padded
+ * buffers that are mostly empty (T*k / E).
+ * `ws` is any workspace of ep_workspace_init of 256 bytes or more (the status
+ * word is all that these calls keep there).
+ * Every entry needs 16-byte aligned row and weight buffers of whole 16-byte
+ * rows, 4-byte aligned binary32 scales, and takes OCP E4M3 codes with one
+ * scale per block of 128 channels in the format scale_fmt
+ * (moedisp_scale_fmt), as dispatch leaves them. */
+typedef struct {
+    int32_t num_experts;      /* E in [1, 4096] */
+    int32_t max_rows;         /* rows of the row buffers, in [0, 2^30) */
+    int32_t expert_stride;    /* 0: contiguous; else rows per expert of the padded layout */
+    int32_t expert_capacity;  /* padded: C >= 0, row_base + C <= expert_stride */
+    int32_t row_base;         /* padded: >= 0 */
+    int32_t expected_rows;    /* >= 0, see above */
+} moedisp_rows;
+
+/* Product of every expert's rows with its weights:
+ *   y[r][n] = sum over blocks b of x_scales[r][b] * w_scales[e][n/128][b] *
+ *             (sum over k in block b of x[r][k] * w[e][n][k]),  e = r's expert,
+ * the two scales multiplied in binary32 first, blocks in ascending order,
+ * accumulated in binary32, rounded once to out_dtype.  fp32 results keep the
+ * products and sums of a block to binary32; for bf16 results a block's sum
+ * comes from the E4M3 matrix instruction, which keeps about 16 bits below the
+ * largest products it adds (1.5e-5 of a result of normal rows, against the
+ * 2e-3 of its rounding to bf16).
+ *   n          columns of y, n % 8 == 0, in [8, 2^20]; the last scale block
+ *              may be cut.
+ *   k          channels of x, k % 128 == 0, in [128, 65536].
+ *   x          E4M3 [max_rows][k], x_scales [max_rows][k/128].
+ *   w          E4M3 [E][n][k], w_scales [E][ceil(n/128)][k/128] (one per
+ *              128 x 128 square).
+ *   y          [max_rows][n] bf16 or fp32 (out_dtype).
+ * The gradient of x is the same call with the transposed weights ([E][k][n],
+ * scales [E][ceil(k/128)][n/128], n % 128 == 0) and the quantised gradient of
+ * y as x.  y must not overlap the inputs.  The order of the sums depends on
+ * the shape only, so equal inputs give equal bits.  NaN codes and scales give
+ * NaN in the sums that hold them.  Status bits: BAD_LAYOUT. */
+int ep_expert_gemm(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale_fmt, const void* x,
+                   const void* x_scales, const void* w, const void* w_scales, const int32_t* row_bounds, void* y,
+                   int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the weights of ep_expert_gemm:
+ *   dw[e][n][k] = sum over e's rows r of dy[r][n] * x_scales[r][k/128] * x[r][k],
+ * plus the previous dw[e][n][k] if accumulate is 1 (fp32 only; 0: dw is
+ * overwritten, with zeros for an expert without rows).
+ *   dy         bf16 [max_rows][n];  x, x_scales as for ep_expert_gemm.
+ *   dw         [E][n][k] bf16 or fp32 (out_dtype).
+ * x_scales[r][b] * x[r][k] is rounded to bf16 (exact for UE8M0 scales from
+ * 2^-116 up), products are exact and sums are binary32, in an order that the
+ * shape and the row bounds give.  Sizes, alignment and status bits as for
+ * ep_expert_gemm. */
+int ep_expert_wgrad(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale_fmt, const void* x,
+                    const void* x_scales, const void* dy, const int32_t* row_bounds, void* dw, int32_t out_dtype,
+                    int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Gated activation with quantisation, between the two products of an expert:
+ *   h[i] = silu(g[i]) * u[i] for gu's row (g[0..inner), u[0..inner)),
+ *   silu(v) = v / (1 + exp(-v)), computed in binary32 and quantised per block
+ * of 128 by the rules of ep_dispatch_quant (scale_fmt FP32 or UE8M0).
+ *   inner     inner % 128 == 0, in [128, 65536].
+ *   gu        bf16 [max_rows][2*inner];  h E4M3 [max_rows][inner];
+ *   h_scales  [max_rows][inner/128] float or uint8.
+ * A block whose largest |h| is infinite or that holds NaN gets NaN codes
+ * (0x7F), with the scale 1.  Status bits: BAD_LAYOUT. */
+int ep_swiglu_quant(const moedisp_rows* rows, int32_t inner, int32_t scale_fmt, const void* gu,
+                    const int32_t* row_bounds, void* h, void* h_scales, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of gu, the quantisation taken as the identity:
+ *   s = 1 / (1 + exp(-g));  dg = dh*u*s*(1 + g*(1-s));  du = dh*g*s
+ *   dh            bf16 [max_rows][inner]
+ *   dgu           bf16 [max_rows][2*inner] (dg, du) or NULL
+ *   dgu_q, dgu_scales  the same gradient before rounding to bf16, quantised
+ *                 as above: E4M3 [max_rows][2*inner] and
+ *                 [max_rows][2*inner/128]; both NULL or both given.
+ * At least one of the two forms is written.  Other arguments as above. */
+int ep_swiglu_backward(const moedisp_rows* rows, int32_t inner, int32_t scale_fmt, const void* gu, const void* dh,
+                       const int32_t* row_bounds, void* dgu, void* dgu_q, void* dgu_scales, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* Scores of the router whose balance is measured. */
+typedef enum {
+    MOEDISP_SCORE_SOFTMAX = 0,  /* p_e = exp(z_e) / sum_j exp(z_j) */
+    MOEDISP_SCORE_SIGMOID = 1   /* p_e = s(z_e) / sum_j s(z_j), s(v) = 1 / (1 + exp(-v)) */
+} moedisp_score;
+
+/* A batch of num_seqs sequences of seq_len tokens each (token s*seq_len + i
+ * is position i of sequence s).  A token all of whose slots are masked (-1)
+ * is padding: it takes no part.  One sequence of all tokens gives the loss
+ * over the whole batch. */
+typedef struct {
+    int32_t num_seqs;      /* S >= 0 */
+    int32_t seq_len;       /* L >= 0, S*L < 2^30 / topk */
+    int32_t num_experts;   /* E in [1, 4096] */
+    int32_t topk;          /* k in [1, 32], k <= E */
+    int32_t score;         /* moedisp_score */
+    int32_t logits_dtype;  /* MOEDISP_BF16 or MOEDISP_FP32 */
+    float coef;            /* finite */
+} moedisp_balance;
+
+/* Bytes of workspace of ep_balance_loss; 0 if the shape is invalid.  At
+ * least 256; initialise it once with ep_workspace_init. */
+size_t ep_balance_workspace_bytes(const moedisp_balance* b);
+
+/* Balance loss of the router over its choices.  With L_s the tokens of
+ * sequence s that have a routed slot, c[s][e] their slots with expert e, p
+ * the scores, and S' the sequences with L_s > 0:
+ *   loss = coef / S' * sum_s sum_e (E * c[s][e] / (k * L_s)) * (1/L_s * sum_t p[t][e])
+ * (0 if S' is 0).
+ *   logits             [S*L][E] bf16 or fp32; -inf scores 0.  A row without
+ *                      a finite logit has p = 0 for all experts.  Rows of padding
+ *                      tokens are not used, whatever they hold.
+ *   topk_idx           int32 [S*L][k], -1 = masked.
+ *   loss               fp32 [1];  tokens_per_expert int32 [S][E] = c;
+ *   tokens_per_seq     int32 [S] = L_s.
+ * Sums are binary32 and fixed in order.  Status bits: BAD_EXPERT_ID. */
+int ep_balance_loss(const moedisp_balance* b, const void* logits, const int32_t* topk_idx, float* loss,
+                    int32_t* tokens_per_expert, int32_t* tokens_per_seq, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the logits: d_logits[t][e] = d_loss * dloss/dz[t][e] in the
+ * type of the logits, 0 for padding tokens; tokens_per_expert and
+ * tokens_per_seq are those that ep_balance_loss left.
+ *   d_loss   fp32 [1], device. */
+int ep_balance_loss_backward(const moedisp_balance* b, const void* logits, const int32_t* topk_idx,
+                             const int32_t* tokens_per_expert, const int32_t* tokens_per_seq, const float* d_loss,
+                             void* d_logits, void* stream);
+
 /* Wait for `stream`, then return the device status bits accumulated in `ws`
  * since the last check in *host_status and clear them. */
 int ep_check_status(void* ws, size_t ws_bytes, void* stream, int32_t* host_status);
