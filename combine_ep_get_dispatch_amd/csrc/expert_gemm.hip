@@ -24,6 +24,7 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7FFFFFFF, kRawBufferWord3);
 }
 
+constexpr int kChunk = 8;  // scale blocks of a row loaded at a time
 constexpr long long kLdsBytes = 160 * 1024;  // of a CU
 
 template <int N>
@@ -31,11 +32,12 @@ __device__ inline void wait_loads_and_sync() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// 32 bytes of an operand row: 16-byte chunks 2q and 2q+1 of the row's 8,
+// 32 bytes of an operand row: 16-byte chunks q and q + 4 of the row's 8,
 // stored at chunk ^ swizzle.
 __device__ inline v8i read_frag(const char* row, int sw, int q) {
-    const v4i lo = *reinterpret_cast<const v4i*>(row + (((2 * q) ^ sw) << 4));
-    const v4i hi = *reinterpret_cast<const v4i*>(row + (((2 * q + 1) ^ sw) << 4));
+    const int lo_at = (q ^ sw) << 4;
+    const v4i lo = *reinterpret_cast<const v4i*>(row + lo_at);
+    const v4i hi = *reinterpret_cast<const v4i*>(row + (lo_at ^ 64));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -70,12 +72,17 @@ struct Tile {
     static constexpr int kNT = kN / 16;
     static constexpr int kWLoads = BN / 8 / kWaves;  // 1 KiB loads of a wave and stage
     static constexpr int kXLoads = (BM / 8 + kWaves - 1) / kWaves;
-    static constexpr int kLoads = kWLoads + kXLoads + 1;
+    static constexpr int kLoads = kWLoads + kXLoads + 1;             // with one load of scales
     static constexpr int kXBytes = kXLoads * kWaves * 1024;
-    static constexpr int kStage = BN * kBlk + kXBytes + kWaves * 256;
+    static constexpr int kStage = BN * kBlk + kXBytes;
+    // scales of the rows: chunks of kChunk blocks, two in LDS, [row][block]
+    static constexpr int kSGroups = BM / 8;                             // loads of 8 rows by kChunk blocks
+    static constexpr int kSTurns = (kSGroups + kWaves - 1) / kWaves;    // blocks in which a chunk is loaded
+    static constexpr int kSBytes = 2 * BM * kChunk * 4 + kWaves * 256;  // and what the other blocks load
+    static_assert(kSTurns + STAGES <= kChunk, "a chunk is there before it is read");
     static constexpr int kSwBlocks = BN >= kBlk ? BN / kBlk : 1;
-    static_assert(kM <= 64 && kM % 16 == 0 && kN % 32 == 0 && kN <= kBlk && BN % (8 * kWaves) == 0, "tile shape");
-    static size_t lds(int kb) { return (size_t)STAGES * kStage + (size_t)kSwBlocks * kb * 4; }
+    static_assert(kNT % 2 == 0 && kM <= 64 && kM % 16 == 0 && kN % 32 == 0 && kN <= kBlk && BN % (8 * kWaves) == 0, "tile shape");
+    static constexpr size_t lds(int kb) { return (size_t)STAGES * kStage + kSBytes + (size_t)kSwBlocks * kb * 4; }
 };
 
 template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
@@ -131,7 +138,14 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         xoff[i] = min(row, rows - 1) * a.k + (((lane & 7) ^ swizzle_x(row)) << 4);
     }
     const int wm = wave % WM, wn = wave / WM;
-    const int soff = min(wm * T::kM + lane, rows - 1) * a.kb * SB;
+    char* const sx_lds = lds + STAGES * T::kStage;
+    // Scales of 8 rows (group g of the tile) and the 8 blocks of chunk ch: 32
+    // bytes of each row at a time, as one scale of 64 rows costs a request
+    // per lane.
+    auto issue_scales = [&](int g, int ch, char* to) {
+        const int at = min(g * 8 + (lane >> 3), rows - 1) * a.kb + min(ch * kChunk + (lane & 7), a.kb - 1);
+        load_to_lds<SB>(srs, to, at * SB, 0);
+    };
 
     auto issue = [&](int kb, int buf) {
         char* st = lds + buf * T::kStage;
@@ -141,12 +155,13 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
 #pragma unroll
         for (int i = 0; i < T::kXLoads; ++i)
             load_to_lds<16>(xrs, st + BN * kBlk + (wave * T::kXLoads + i) * 1024, xoff[i], kb * kBlk);
-        load_to_lds<SB>(srs, st + BN * kBlk + T::kXBytes + wave * 256, soff, kb * SB);
     };
 
-    __syncthreads();  // the last tile's reads of LDS are done
+    wait_loads_and_sync<0>();  // the last tile's loads into LDS and reads of it are done
+    char* const unused = sx_lds + 2 * BM * kChunk * 4 + wave * 256;
+
     // the weights' scales of the tile, all of k
-    int* sw = reinterpret_cast<int*>(lds + STAGES * T::kStage);
+    int* sw = reinterpret_cast<int*>(sx_lds + T::kSBytes);
     for (int i = tid; i < T::kSwBlocks * a.kb; i += T::kThreads) {
         const int b = i / a.kb;
         const size_t at = ((size_t)s.e * a.nb + min(n0 / kBlk + b, a.nb - 1)) * a.kb + (i - b * a.kb);
@@ -162,65 +177,98 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         for (int j = 0; j < T::kMT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
 #pragma unroll
-    for (int p = 0; p < STAGES - 1; ++p)
-        if (p < a.kb) issue(p, p);
+    for (int t = 0; t < T::kSTurns; ++t)
+        if (t * T::kWaves + wave < T::kSGroups)
+            issue_scales(t * T::kWaves + wave, 0, sx_lds + (t * T::kWaves + wave) * 256);
+#pragma unroll
+    for (int p = 0; p < STAGES; ++p) {
+        issue(min(p, a.kb - 1), p);
+        issue_scales(0, 0, unused);  // as many loads as a later block has
+    }
 
     const int q = lane >> 4, c = lane & 15;
     const int wrow = wn * T::kN + (c >> 2) * 8 + (c & 3);
     const int xrow = wm * T::kM + c;
     const int wsw = swizzle_w(wrow), xsw = swizzle_x(xrow);
-    int buf = 0, nbuf = STAGES - 1;
-    for (int kb = 0; kb < a.kb; ++kb) {
-        if (kb + STAGES - 1 < a.kb) {
-            wait_loads_and_sync<(STAGES - 2) * T::kLoads>();
-            issue(kb + STAGES - 1, nbuf);
-        } else {
-            wait_loads_and_sync<0>();
-        }
-        const char* st = lds + buf * T::kStage;
-        const char* wt = st + wrow * kBlk;
-        const char* xt = st + BN * kBlk + xrow * kBlk;
-        const int* sx = reinterpret_cast<const int*>(st + BN * kBlk + T::kXBytes + wave * 256);
-        const int swv = swp[kb];
-        v8i b[T::kMT];
-        int sxv[T::kMT];
+    // scale of the block's partial sums; the power-of-two scales of bf16
+    // results go into the matrix instruction
+    constexpr bool PROMOTE = FMT == MOEDISP_SCALE_FP32 || F32;
+    v8i b[T::kMT], wf[2];
+    int sxv[T::kMT];
+    auto w_at = [&](const char* st, int i) {
+        return read_frag(st + (wrow + (i >> 1) * 32 + (i & 1) * 4) * kBlk, wsw, q);
+    };
+    auto x_at = [&](const char* st, int kb, int j) {
+        sxv[j] = reinterpret_cast<const int*>(
+            sx_lds)[(((kb / kChunk) & 1) * BM + wm * T::kM + j * 16 + c) * kChunk + kb % kChunk];
+        return read_frag(st + BN * kBlk + (xrow + j * 16) * kBlk, xsw, q);
+    };
+    wait_loads_and_sync<(STAGES - 1) * T::kLoads>();
+    wf[0] = w_at(lds, 0);
 #pragma unroll
-        for (int j = 0; j < T::kMT; ++j) {
-            b[j] = read_frag(xt + j * 16 * kBlk, xsw, q);
-            sxv[j] = sx[j * 16 + c];
-        }
-        // scale of the block's partial sums; the power-of-two scales of bf16
-        // results go into the matrix instruction
-        constexpr bool PROMOTE = FMT == MOEDISP_SCALE_FP32 || F32;
+    for (int j = 0; j < T::kMT; ++j) b[j] = x_at(lds, 0, j);
+    // Block kb: its rows' operands and the first of the weights' are in
+    // registers.  Product u = (i, j) is followed by the scaled add of the
+    // product LAG before it, so that the matrix unit need not finish one
+    // first; sched_barrier keeps this order.  Before the last i the block's
+    // LDS has been read: the waves meet, its place is filled with the block
+    // STAGES later, and the next block's operands are read behind the last
+    // products.
+    int buf = 0;
+    for (int kb = 0; kb < a.kb; ++kb) {
+        const char* st = lds + buf * T::kStage;
+        const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
+        const char* nst = lds + nbuf * T::kStage;
+        const int swv = swp[kb];
         float f[T::kMT];
         if (PROMOTE) {
 #pragma unroll
             for (int j = 0; j < T::kMT; ++j) f[j] = scale_value<FMT>(sxv[j]) * scale_value<FMT>(swv);
         }
+        constexpr int LAG = 2;
+        constexpr int U = T::kNT * T::kMT;
+        v4f p[LAG + 1];
 #pragma unroll
-        for (int i = 0; i < T::kNT; ++i) {
-            const v8i w = read_frag(wt + ((i >> 1) * 32 + (i & 1) * 4) * kBlk, wsw, q);
-#pragma unroll
-            for (int j = 0; j < T::kMT; ++j) {
-                if (PROMOTE) {
-                    v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (F32) {
-#pragma unroll
-                        for (int h = 0; h < 4; ++h)
-                            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w, h), widen(b[j], h), p, 0, 0, 0);
-                    } else {
-                        p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, b[j], p, 0, 0, 0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[i][j][v] = __builtin_fmaf(p[v], f[j], acc[i][j][v]);
-                } else {
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, b[j], acc[i][j], 0, 0, 0, swv, 0,
-                                                                                 sxv[j]);
+        for (int u = 0; u < U + LAG; ++u) {
+            const int i = u / T::kMT, j = u % T::kMT;
+            if (u < U) {
+                if (j == 0 && i + 1 < T::kNT) wf[(i + 1) & 1] = w_at(st, i + 1);
+                if (u == U - T::kMT) {
+                    wait_loads_and_sync<(STAGES - 2) * T::kLoads>();
+                    issue(min(kb + STAGES, a.kb - 1), buf);
+                    // the next chunk of the rows' scales, in the first blocks
+                    // of this one; later blocks load to a place of no use, so
+                    // that every block has as many loads to wait for
+                    const int g = kb % kChunk * T::kWaves + wave;
+                    issue_scales(min(g, T::kSGroups - 1), kb / kChunk + 1,
+                                 g < T::kSGroups ? sx_lds + (kb / kChunk + 1) % 2 * BM * kChunk * 4 + g * 256 : unused);
+                    __builtin_amdgcn_sched_barrier(0);
+                    wf[0] = w_at(nst, 0);
                 }
+                if (!PROMOTE) {
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i & 1], b[j], acc[i][j], 0, 0, 0,
+                                                                                 swv, 0, sxv[j]);
+                } else if (F32) {
+                    v4f r = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                        r = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(wf[i & 1], h), widen(b[j], h), r, 0, 0, 0);
+                    p[u % (LAG + 1)] = r;
+                } else {
+                    p[u % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        wf[i & 1], b[j], v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+                }
+                if (u >= U - T::kMT) b[j] = x_at(nst, kb + 1, j);
             }
+            if (PROMOTE && u >= LAG) {
+                const int io = (u - LAG) / T::kMT, jo = (u - LAG) % T::kMT;
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    acc[io][jo][v] = __builtin_fmaf(p[(u - LAG) % (LAG + 1)][v], f[jo], acc[io][jo][v]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        buf = buf + 1 == STAGES ? 0 : buf + 1;
-        nbuf = nbuf + 1 == STAGES ? 0 : nbuf + 1;
+        buf = nbuf;
     }
 
 #pragma unroll
@@ -253,6 +301,7 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
     a.nt = (a.n + BN - 1) / BN;
     const long long tiles = (long long)a.r.max_rows / BM + a.r.E;  // at least the tiles of any bounds
     if (tiles * a.nt > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
+    static_assert(T::lds(512) <= kLdsBytes, "65536 channels");
     const size_t lds = T::lds(a.kb);
     long long blocks = (tiles * a.nt + kXcds - 1) / kXcds * kXcds;
     const long long resident = 256 * (kLdsBytes / (long long)lds);
@@ -262,9 +311,19 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Tile by the rows an expert usually has.  Few rows: every weight is read
+// once per row tile whatever its height, so the tile is as flat as the rows
+// allow and several workgroups share a compute unit; many rows: the tile
+// whose loads per product are fewest.
 template <int FMT, bool F32>
 hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
-    return launch_tile<64, 128, 1, 4, 2, FMT, F32>(a, stream);
+    if (mean_rows <= 8) return launch_tile<16, 128, 1, 4, 4, FMT, F32>(a, stream);
+    if (mean_rows <= 24) return launch_tile<32, 128, 1, 4, 3, FMT, F32>(a, stream);
+    if (mean_rows <= 48) return launch_tile<64, 256, 1, 4, 3, FMT, F32>(a, stream);
+    // (fp32 results keep widened operands in registers: the largest tile would spill)
+    if (mean_rows <= 192 || F32) return launch_tile<128, 256, 2, 4, 3, FMT, F32>(a, stream);
+    if constexpr (!F32) return launch_tile<256, 256, 4, 2, 2, FMT, F32>(a, stream);
+    return hipErrorInvalidConfiguration;  // not reached
 }
 
 }  // namespace
