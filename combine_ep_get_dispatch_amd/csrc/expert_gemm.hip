@@ -8,29 +8,8 @@ namespace {
 
 constexpr int kBlk = kScaleBlock;
 
-// Loads of `SIZE` bytes per lane straight into LDS at `lds` + lane * max(4, SIZE).
-template <int SIZE>
-__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t rs, char* lds, int voff, int soff) {
-    auto* to = (__attribute__((address_space(3))) void*)lds;
-    if constexpr (SIZE == 16)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, voff, soff, 0, 0);
-    else if constexpr (SIZE == 4)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 4, voff, soff, 0, 0);
-    else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 1, voff, soff, 0, 0);
-}
-
-__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7FFFFFFF, kRawBufferWord3);
-}
-
 constexpr int kChunk = 8;  // scale blocks of a row loaded at a time
 constexpr long long kLdsBytes = 160 * 1024;  // of a CU
-
-template <int N>
-__device__ inline void wait_loads_and_sync() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
 
 // 32 bytes of an operand row: 16-byte chunks q and q + 4 of the row's 8,
 // stored at chunk ^ swizzle.
@@ -293,6 +272,7 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         }
     }
     }
+    wait_loads_and_sync<0>();  // no load may reach LDS after the workgroup's end
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>

@@ -6,206 +6,227 @@ namespace moedisp {
 namespace {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
 
-constexpr int kT = 256;     // tile: 256 columns of dy by 256 channels of x
-constexpr int kStep = 32;   // rows per step
-constexpr int kWaves = 8;   // waves 0..3 stage dy, 4..7 stage x; each multiplies 64 columns by 128 channels
+constexpr int kStep = 32;    // rows per step: the contraction of one matrix instruction
+constexpr int kStages = 4;   // steps of dy in LDS, and of x in registers
 
-// Position of column (or channel) i of the tile among the 256 16-byte units
-// of one group of 8 rows.  A lane that stages writes units 4l..4l+3 and the
-// operand reads take 16 units whose low bits run over {0,1,2,3} or {0,1,3,4}:
-// mixing bits 4 and 5 into the low ones puts 16 neighbouring lanes of either
-// on 16 different units modulo 16, so that no two share LDS banks.
-__device__ inline int unit_of(int i) { return i ^ ((i & 16) ? 5 : 0) ^ ((i & 32) ? 2 : 0); }
+// In LDS both operands lie by rows, in bf16, as units of 32 bytes (16 columns
+// or channels); unit u of row r is stored at u ^ unit_swizzle(r).  An operand
+// read takes the same unit of 4 rows for each of 4 groups of 16 lanes (rows r,
+// r + 8, r + 16, r + 24): the swizzle puts 8 of these 16 on different banks,
+// as many as 64 banks hold.
+__device__ inline int unit_swizzle(int r) { return (r & 3) | ((r >> 1) & 4); }
 
-__device__ inline uint32_t perm_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
-__device__ inline uint32_t perm_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
-
-// Scale number `at` where it is the same in all lanes: a scalar load (of the
-// aligned word that holds it).
-template <int FMT>
-__device__ inline float uniform_scale(const void* p, size_t at) {
-    typedef const __attribute__((address_space(4))) uint32_t* cptr;
-    if (FMT == MOEDISP_SCALE_FP32) return __uint_as_float(((cptr)(uintptr_t)p)[at]);
-    const uintptr_t b = (uintptr_t)p + at;
-    return ue8m0_value((*(cptr)(b & ~(uintptr_t)3) >> ((b & 3) * 8)) & 255u);
+// Lane 4m + i of 16 reads 8 bytes of row m of four; lane c gets column c of
+// the 16 that the four rows' pieces make up, a row each.
+__device__ inline v4s read_transposed(const char* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
 }
 
-template <int FMT, bool F32, bool ADD>
-__global__ __launch_bounds__(64 * kWaves) void moedisp_expert_wgrad(ExpertWgradArgs a) {
-    __shared__ v4u lds[2][2][kStep / 8][kT];  // [buffer][dy, x][rows / 8][unit]
+// Tile of TN columns of dy by TK channels of x; WN x WK waves.
+template <int TN, int TK, int WN, int WK>
+struct WTile {
+    static constexpr int kWaves = WN * WK;
+    static constexpr int kThreads = 64 * kWaves;
+    static constexpr int kNT = TN / WN / 16;   // 16-wide tiles of a wave
+    static constexpr int kKT = TK / WK / 16;
+    static constexpr int kDyRow = TN * 2;      // bytes
+    static constexpr int kXRow = TK * 2;
+    static constexpr int kDyStage = kStep * kDyRow;
+    static constexpr int kXStage = kStep * kXRow;
+    static constexpr int kDyLoads = kDyStage / 1024 / kWaves;  // of a wave and step
+    static constexpr int kXLanes = TK / 16;                    // lanes of a row, 16 channels each
+    static constexpr int kXRows = 64 / kXLanes;                // rows of a wave and step
+    static constexpr int kOps = kDyLoads + 2;                  // loads of a wave and step
+    static constexpr int kLds = kStages * kDyStage + 2 * kXStage;
+    static_assert(kXRows * kWaves == kStep && kDyRow >= 256 && kXRow >= 256, "tile shape");
+};
+
+template <int TN, int TK, int WN, int WK, int FMT, bool F32, bool ADD>
+__global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgradArgs a) {
+    using T = WTile<TN, TK, WN, WK>;
+    extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     int incl, own;
-    const int rows_total = expert_tiles<1>(a.r, &incl, &own);
-    if (rows_total < 0) {
+    if (expert_tiles<1>(a.r, &incl, &own) < 0) {
         if (blockIdx.x == 0 && tid == 0) atomicOr(&a.hdr->status, (uint32_t)MOEDISP_DEV_BAD_LAYOUT);
         return;
     }
+    // XCD x (consecutive workgroups go round the XCDs) takes every 8th run of
+    // kRun tiles, neighbours of kGroup column tiles by kRun / kGroup channel
+    // tiles that share their rows in its L2.  Short runs: experts' rows are
+    // uneven, and so is the work of a run.
+    constexpr int kRun = 32, kGroup = 4;
+    const int local = blockIdx.x / kXcds;
+    const long long item = ((long long)(local / kRun) * kXcds + blockIdx.x % kXcds) * kRun + local % kRun;
     const int per_expert = a.nt * a.kt;
-    const int e = blockIdx.x / per_expert;
-    const int rest = blockIdx.x - e * per_expert;
-    const int n0 = (rest / a.kt) * kT, k0 = (rest % a.kt) * kT;
+    if (item >= (long long)a.r.E * per_expert) return;
+    const int e = (int)(item / per_expert);
+    const int rest = (int)(item - (long long)e * per_expert);
+    const int grp = rest / (kGroup * a.kt);
+    const int gn = min(kGroup, a.nt - grp * kGroup);
+    const int in_grp = rest - grp * kGroup * a.kt;
+    const int n0 = (grp * kGroup + in_grp % gn) * TN, k0 = (in_grp / gn) * TK;
     int first, rows;
     expert_rows(a.r, e, a.r.bounds[e], a.r.bounds[a.r.stride > 0 ? e : e + 1], &first, &rows);
     first = __builtin_amdgcn_readfirstlane(first);
     rows = __builtin_amdgcn_readfirstlane(rows);
-
-    // Staging: a wave takes 8 rows of a step; a lane 4 columns of dy or 4
-    // channels of x.  Rows past the expert's last lie past the end of the
-    // step's buffer and read as zero; columns past a row's end hold what
-    // follows in memory and go into results that are not stored.
-    const bool is_x = wave >= 4;
-    const int g = wave & 3;
-    const int c4 = 4 * lane;
-    const int rb = is_x ? a.k : a.n * 2;  // bytes of a row
-    const int c0 = is_x ? k0 + c4 : (n0 + c4) * 2;
-    v2i d[2][8];
-    float sc[2][8][2];
     const int steps = (rows + kStep - 1) / kStep;
-    auto load = [&](int step, int u) {
-        if (step >= steps) return;
-        const int r0 = step * kStep + g * 8;
-        const int left = max(0, min(8, rows - r0));
-        const size_t row = (size_t)first + min(r0, rows - 1);
-        const char* base = (is_x ? (const char*)a.x : (const char*)a.dy) + row * rb;
-        const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, left * rb, kRawBufferWord3);
-        if (is_x) {
+
+    // dy: rows as they are, straight into LDS.  Load i of the wave brings
+    // 1 KiB; rows past the expert's last are read as its last, and count
+    // nothing as x is zero there.
+    int dy_row[T::kDyLoads], dy_col[T::kDyLoads];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[u][i].x = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, c0 + i * rb, 0, 0);
-            // the two scales of each row that the tile spans, by scalar loads
+    for (int i = 0; i < T::kDyLoads; ++i) {
+        const int at = (wave * T::kDyLoads + i) * 1024 + lane * 16;
+        dy_row[i] = at / T::kDyRow;
+        const int chunk = (at % T::kDyRow / 16) ^ (unit_swizzle(dy_row[i]) << 1);
+        dy_col[i] = min(chunk * 16, (a.n - n0) * 2 - 16);
+    }
+    auto load_dy = [&](int step, int buf) {
+        const int r0 = min(step * kStep, rows - 1);
+        const char* base = (const char*)a.dy + (((size_t)first + r0) * a.n + n0) * 2;
+        const auto rs = buffer_of(base);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const size_t at = ((size_t)first + min(r0 + i, rows - 1)) * a.kb;
-                const int b0 = k0 / kScaleBlock, b1 = min(b0 + 1, a.kb - 1);
-                sc[u][i][0] = uniform_scale<FMT>(a.x_scales, at + b0);
-                sc[u][i][1] = uniform_scale<FMT>(a.x_scales, at + b1);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                d[u][i] = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rs, c0 + i * rb, 0, 0));
-        }
+        for (int i = 0; i < T::kDyLoads; ++i)
+            load_to_lds<16>(rs, lds + buf * T::kDyStage + (wave * T::kDyLoads + i) * 1024,
+                            min(dy_row[i], rows - 1 - r0) * (a.n * 2) + dy_col[i], 0);
     };
-    auto stage = [&](int step, int u) {
-        if (step >= steps) return;
-        v4u o[4];
-        if (is_x) {
-            const bool second = lane >= 32;
+    // x: 16 channels of a row per lane through registers, where they become
+    // bf16 (scale times code, rounded once); zero past the expert's last row
+    v4u xr[kStages];
+    int xs[kStages];
+    const int x_row = wave * T::kXRows + lane / T::kXLanes;
+    const int x_ch = min(k0 + lane % T::kXLanes * 16, a.k - 16);
+    auto load_x = [&](int step, int u) {
+        const int r0 = min(step * kStep, rows - 1);
+        const size_t row = (size_t)first + r0 + min(x_row, rows - 1 - r0);
+        xr[u] = *reinterpret_cast<const v4u*>(a.x + row * a.k + x_ch);
+        const size_t at = row * a.kb + x_ch / kScaleBlock;
+        xs[u] = FMT == MOEDISP_SCALE_FP32 ? reinterpret_cast<const int*>(a.x_scales)[at]
+                                          : (int)reinterpret_cast<const uint8_t*>(a.x_scales)[at];
+    };
+    char* const x_lds = lds + kStages * T::kDyStage;
+    const int x_at = x_row * T::kXRow + ((lane % T::kXLanes) ^ unit_swizzle(x_row)) * 32;
+    const int x_half = (lane >> 3) & 1;  // of the 32 bytes, which 16 first: 8 neighbours fill different banks
+    auto stage_x = [&](int step, int u) {
+        const float s = FMT == MOEDISP_SCALE_FP32 ? __int_as_float(xs[u]) : ue8m0_value((uint32_t)xs[u]);
+        const bool on = step * kStep + x_row < rows;
+        v4u o[2];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const v2f lo0 = __builtin_amdgcn_cvt_pk_f32_fp8(d[u][2 * p].x, false);
-                const v2f hi0 = __builtin_amdgcn_cvt_pk_f32_fp8(d[u][2 * p].x, true);
-                const v2f lo1 = __builtin_amdgcn_cvt_pk_f32_fp8(d[u][2 * p + 1].x, false);
-                const v2f hi1 = __builtin_amdgcn_cvt_pk_f32_fp8(d[u][2 * p + 1].x, true);
-                const int r = step * kStep + g * 8 + 2 * p;
-                const float s0 = r < rows ? (second ? sc[u][2 * p][1] : sc[u][2 * p][0]) : 0.0f;
-                const float s1 = r + 1 < rows ? (second ? sc[u][2 * p + 1][1] : sc[u][2 * p + 1][0]) : 0.0f;
-                o[0][p] = pack_bf16x2(lo0.x * s0, lo1.x * s1);
-                o[1][p] = pack_bf16x2(lo0.y * s0, lo1.y * s1);
-                o[2][p] = pack_bf16x2(hi0.x * s0, hi1.x * s1);
-                o[3][p] = pack_bf16x2(hi0.y * s0, hi1.y * s1);
-            }
-        } else {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const v2i r0 = d[u][2 * p], r1 = d[u][2 * p + 1];
-                o[0][p] = perm_lo(r0.x, r1.x);
-                o[1][p] = perm_hi(r0.x, r1.x);
-                o[2][p] = perm_lo(r0.y, r1.y);
-                o[3][p] = perm_hi(r0.y, r1.y);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[u][i], false);
+            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[u][i], true);
+            o[i >> 1][2 * (i & 1)] = on ? pack_bf16x2(lo.x * s, lo.y * s) : 0u;
+            o[i >> 1][2 * (i & 1) + 1] = on ? pack_bf16x2(hi.x * s, hi.y * s) : 0u;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds[step & 1][is_x ? 1 : 0][g][unit_of(c4 + i)] = o[i];
+        char* to = x_lds + (step & 1) * T::kXStage + x_at;
+        *reinterpret_cast<v4u*>(to + x_half * 16) = x_half ? o[1] : o[0];
+        *reinterpret_cast<v4u*>(to + (x_half ^ 1) * 16) = x_half ? o[0] : o[1];
     };
 
-    constexpr int kKT = 8, kNT = 4;  // 16-wide tiles of a wave: channels, columns
-    const int wk = (wave & 1) * 128, wn = (wave >> 1) * 64;
-    v4f acc[kKT][kNT];
+    const int wk = wave % WK * (TK / WK), wn = wave / WK * (TN / WN);
+    v4f acc[T::kKT][T::kNT];
 #pragma unroll
-    for (int i = 0; i < kKT; ++i)
+    for (int i = 0; i < T::kKT; ++i)
 #pragma unroll
-        for (int j = 0; j < kNT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < T::kNT; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int q = lane >> 4, c = lane & 15;
-    load(0, 0);
-    load(1, 1);
-    stage(0, 0);
-    load(2, 0);
-    for (int s0 = 0; s0 < steps; s0 += 2) {
+    // the lane's place in the transposing reads of rows 8q + c/4 (and + 4)
+    const int tr_row = q * 8 + (c >> 2);
+    const int tr_sw = unit_swizzle(tr_row);  // the same 4 rows below
+    // 8 rows of column (or channel) c of unit u
+    auto operand = [&](const char* st, int row_bytes, int u) {
+        const char* p = st + tr_row * row_bytes + ((u ^ tr_sw) << 5) + ((c & 3) << 3);
+        const v4s lo = read_transposed(p);
+        const v4s hi = read_transposed(p + 4 * row_bytes);
+        return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+
+    if (steps > 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int s = s0 + h;
-            if (s >= steps) break;
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            // the waves of x have the conversions: they stage before their
-            // products, those of dy behind them, so that one of the two waves
-            // of a SIMD unit keeps the matrix unit busy
-            if (is_x) {
-                stage(s + 1, h ^ 1);
-                load(s + 3, h ^ 1);
-            }
-            v8bf b[kNT];
+        for (int p = 0; p < kStages; ++p) {
+            load_x(p, p);
+            if (p < kStages - 1) load_dy(p, p);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage_x(0, 0);
+        wait_loads_and_sync<(kStages - 2) * T::kOps>();
+        for (int s0 = 0; s0 < steps; s0 += kStages) {
 #pragma unroll
-            for (int j = 0; j < kNT; ++j) b[j] = __builtin_bit_cast(v8bf, lds[h][0][q][unit_of(wn + j * 16 + c)]);
+            for (int h = 0; h < kStages; ++h) {
+                const int s = s0 + h;
+                if (s >= steps) break;
+                load_x(s + kStages, h);
+                load_dy(s + kStages - 1, (h + kStages - 1) % kStages);
+                __builtin_amdgcn_sched_barrier(0);
+                stage_x(s + 1, (h + 1) % kStages);
+                const char* ds = lds + h * T::kDyStage;
+                const char* xst = x_lds + (h & 1) * T::kXStage;
+                v8bf b[T::kNT], av[2];
 #pragma unroll
-            for (int i = 0; i < kKT; ++i) {
-                const int ch = wk + (i >> 1) * 32 + (c >> 2) * 8 + (i & 1) * 4 + (c & 3);
-                const v8bf av = __builtin_bit_cast(v8bf, lds[h][1][q][unit_of(ch)]);
+                for (int j = 0; j < T::kNT; ++j) b[j] = operand(ds, T::kDyRow, wn / 16 + j);
+                av[0] = operand(xst, T::kXRow, wk / 16);
 #pragma unroll
-                for (int j = 0; j < kNT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, b[j], acc[i][j], 0, 0, 0);
-            }
-            if (!is_x) {
-                stage(s + 1, h ^ 1);
-                load(s + 3, h ^ 1);
+                for (int i = 0; i < T::kKT; ++i) {
+                    if (i + 1 < T::kKT) av[(i + 1) & 1] = operand(xst, T::kXRow, wk / 16 + i + 1);
+#pragma unroll
+                    for (int j = 0; j < T::kNT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1], b[j], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                wait_loads_and_sync<(kStages - 2) * T::kOps>();
             }
         }
+        wait_loads_and_sync<0>();  // no load may reach LDS after the workgroup's end
     }
 
 #pragma unroll
-    for (int j = 0; j < kNT; ++j) {
+    for (int j = 0; j < T::kNT; ++j) {
         const int n = n0 + wn + j * 16 + c;
         if (n >= a.n) continue;
 #pragma unroll
-        for (int t = 0; t < kKT / 2; ++t) {
-            const int k = k0 + wk + t * 32 + q * 8;
+        for (int i = 0; i < T::kKT; ++i) {
+            const int k = k0 + wk + i * 16 + q * 4;
             if (k >= a.k) continue;
             const size_t at = ((size_t)e * a.n + n) * a.k + k;
-            v4f lo = acc[2 * t][j], hi = acc[2 * t + 1][j];
+            v4f v = acc[i][j];
             if (F32) {
                 v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.dw) + at);
-                if (ADD) {
-                    lo += o[0];
-                    hi += o[1];
-                }
-                o[0] = lo;
-                o[1] = hi;
+                if (ADD) v += *o;
+                *o = v;
             } else {
-                const v4u v = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
-                               pack_bf16x2(hi[2], hi[3])};
-                *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.dw) + at) = v;
+                *reinterpret_cast<v2i*>(reinterpret_cast<uint16_t*>(a.dw) + at) =
+                    v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
             }
         }
     }
 }
 
-template <int FMT, bool F32, bool ADD>
+template <int TN, int TK, int WN, int WK, int FMT, bool F32, bool ADD>
 hipError_t launch_one(ExpertWgradArgs a, hipStream_t stream) {
-    a.nt = (a.n + kT - 1) / kT;
-    a.kt = (a.k + kT - 1) / kT;
-    const long long blocks = (long long)a.r.E * a.nt * a.kt;
-    if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((moedisp_expert_wgrad<FMT, F32, ADD>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
+    using T = WTile<TN, TK, WN, WK>;
+    a.nt = (a.n + TN - 1) / TN;
+    a.kt = (a.k + TK - 1) / TK;
+    const long long blocks = ((long long)a.r.E * a.nt * a.kt + 255) / 256 * 256;  // whole runs of 32 on each XCD
+    if (!grid_fits(blocks, T::kThreads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((moedisp_expert_wgrad<TN, TK, WN, WK, FMT, F32, ADD>), dim3((unsigned)blocks),
+                       dim3(T::kThreads), T::kLds, stream, a);
     return hipGetLastError();
 }
 
+#ifndef WTILE
+#define WTILE 256, 256, 4, 2
+#endif
 template <int FMT>
 hipError_t launch_fmt(const ExpertWgradArgs& a, bool f32_out, bool accumulate, hipStream_t stream) {
-    if (!f32_out) return launch_one<FMT, false, false>(a, stream);
-    return accumulate ? launch_one<FMT, true, true>(a, stream) : launch_one<FMT, true, false>(a, stream);
+    if (!f32_out) return launch_one<WTILE, FMT, false, false>(a, stream);
+    return accumulate ? launch_one<WTILE, FMT, true, true>(a, stream) : launch_one<WTILE, FMT, true, false>(a, stream);
 }
 
 }  // namespace

@@ -51,6 +51,29 @@ __device__ inline float ue8m0_value(uint32_t b) {
 __device__ inline float bf16_low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ inline float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// Loads of `SIZE` bytes per lane straight into LDS at `lds` + lane * max(4, SIZE).
+template <int SIZE>
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t rs, char* lds, int voff, int soff) {
+    auto* to = (__attribute__((address_space(3))) void*)lds;
+    if constexpr (SIZE == 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, voff, soff, 0, 0);
+    else if constexpr (SIZE == 4)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 4, voff, soff, 0, 0);
+    else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 1, voff, soff, 0, 0);
+}
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, 0x7FFFFFFF, kRawBufferWord3);
+}
+
+// Waits until at most N of the wave's loads are under way and its LDS accesses
+// are done, then for the workgroup.  (A plain barrier would wait for all loads.)
+template <int N>
+__device__ inline void wait_loads_and_sync() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // First row and number of rows of expert e, from its bounds (b1 is not used
 // in the padded layout); false if they break the rules.
 __device__ inline bool expert_rows(const RowsArg& r, int e, int b0, int b1, int* first, int* count) {
