@@ -9,7 +9,7 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 32;    // rows per step: the contraction of one matrix instruction
-constexpr int kStages = 4;   // steps of dy in LDS, and of x in registers
+constexpr int kStages = 4;   // steps under way or in use
 
 // In LDS both operands lie by rows, in bf16, as units of 32 bytes (16 columns
 // or channels); unit u of row r is stored at u ^ unit_swizzle(r).  An operand
@@ -22,6 +22,37 @@ __device__ inline int unit_swizzle(int r) { return (r & 3) | ((r >> 1) & 4); }
 // the 16 that the four rows' pieces make up, a row each.
 __device__ inline v4s read_transposed(const char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
+}
+
+// load_to_lds (experts_common.h) by an instruction that the compiler does not
+// see into: with the builtin it waits for every load into LDS before a
+// transposing read, and nothing could be loaded ahead (1372 us against 1115
+// for 4096 x 4096 weights and 32768 rows).  There is no result register; the
+// waits are wait_loads_and_sync's and wait_own_loads'.  The leading s_nop
+// covers a descriptor that a vector instruction has just written.
+template <int SIZE>
+__device__ inline void load_to_lds_unseen(const void* base, const char* lds, int voff) {
+    const uint32_t to = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds;
+    const v4i rs = {__builtin_amdgcn_readfirstlane((int)(uintptr_t)base),
+                    __builtin_amdgcn_readfirstlane((int)((uintptr_t)base >> 32) & 0xFFFF), 0x7FFFFFFF, kRawBufferWord3};
+    if constexpr (SIZE == 16)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+                     "v"(voff), "s"(rs)
+                     : "memory");
+    else if constexpr (SIZE == 4)
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
+                     "v"(voff), "s"(rs)
+                     : "memory");
+    else
+        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(to),
+                     "v"(voff), "s"(rs)
+                     : "memory");
+}
+
+// At most N of the wave's own loads are under way.
+template <int N>
+__device__ inline void wait_own_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // Tile of TN columns of dy by TK channels of x; WN x WK waves.
@@ -39,8 +70,9 @@ struct WTile {
     static constexpr int kXLanes = TK / 16;                    // lanes of a row, 16 channels each
     static constexpr int kXRows = 64 / kXLanes;                // rows of a wave and step
     static constexpr int kOps = kDyLoads + 2;                  // loads of a wave and step
-    static constexpr int kLds = kStages * kDyStage + 2 * kXStage;
-    static_assert(kXRows * kWaves == kStep && kDyRow >= 256 && kXRow >= 256, "tile shape");
+    static constexpr int kXRaw = 1024 + 256;                   // a wave's codes and scales of a step
+    static constexpr int kLds = kStages * (kDyStage + kWaves * kXRaw) + 2 * kXStage;
+    static_assert(kKT >= 4 && kXRows * kWaves == kStep && kDyRow >= 256 && kXRow >= 256, "tile shape");
 };
 
 template <int TN, int TK, int WN, int WK, int FMT, bool F32, bool ADD>
@@ -91,39 +123,40 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
     auto load_dy = [&](int step, int buf) {
         const int r0 = min(step * kStep, rows - 1);
         const char* base = (const char*)a.dy + (((size_t)first + r0) * a.n + n0) * 2;
-        const auto rs = buffer_of(base);
 #pragma unroll
         for (int i = 0; i < T::kDyLoads; ++i)
-            load_to_lds<16>(rs, lds + buf * T::kDyStage + (wave * T::kDyLoads + i) * 1024,
-                            min(dy_row[i], rows - 1 - r0) * (a.n * 2) + dy_col[i], 0);
+            load_to_lds_unseen<16>(base, lds + buf * T::kDyStage + (wave * T::kDyLoads + i) * 1024,
+                                   min(dy_row[i], rows - 1 - r0) * (a.n * 2) + dy_col[i]);
     };
-    // x: 16 channels of a row per lane through registers, where they become
-    // bf16 (scale times code, rounded once); zero past the expert's last row
-    v4u xr[kStages];
-    int xs[kStages];
+    // x: 16 channels of a row and their scale per lane, to a place of the
+    // wave's own; from there they become bf16 (scale times code, rounded
+    // once), zero past the expert's last row
+    constexpr int SB = FMT == MOEDISP_SCALE_FP32 ? 4 : 1;
+    char* const raw = lds + kStages * T::kDyStage + 2 * T::kXStage + wave * (kStages * T::kXRaw);
     const int x_row = wave * T::kXRows + lane / T::kXLanes;
     const int x_ch = min(k0 + lane % T::kXLanes * 16, a.k - 16);
     auto load_x = [&](int step, int u) {
         const int r0 = min(step * kStep, rows - 1);
-        const size_t row = (size_t)first + r0 + min(x_row, rows - 1 - r0);
-        xr[u] = *reinterpret_cast<const v4u*>(a.x + row * a.k + x_ch);
-        const size_t at = row * a.kb + x_ch / kScaleBlock;
-        xs[u] = FMT == MOEDISP_SCALE_FP32 ? reinterpret_cast<const int*>(a.x_scales)[at]
-                                          : (int)reinterpret_cast<const uint8_t*>(a.x_scales)[at];
+        const int row = min(x_row, rows - 1 - r0);
+        load_to_lds_unseen<16>(a.x + ((size_t)first + r0) * a.k, raw + u * T::kXRaw, row * a.k + x_ch);
+        load_to_lds_unseen<SB>((const char*)a.x_scales + ((size_t)first + r0) * a.kb * SB, raw + u * T::kXRaw + 1024,
+                               (row * a.kb + x_ch / kScaleBlock) * SB);
     };
     char* const x_lds = lds + kStages * T::kDyStage;
     const int x_at = x_row * T::kXRow + ((lane % T::kXLanes) ^ unit_swizzle(x_row)) * 32;
     const int x_half = (lane >> 3) & 1;  // of the 32 bytes, which 16 first: 8 neighbours fill different banks
     auto stage_x = [&](int step, int u) {
-        const float s = FMT == MOEDISP_SCALE_FP32 ? __int_as_float(xs[u]) : ue8m0_value((uint32_t)xs[u]);
-        const bool on = step * kStep + x_row < rows;
+        const v4u xr = *reinterpret_cast<const v4u*>(raw + u * T::kXRaw + lane * 16);
+        const int xs = *reinterpret_cast<const int*>(raw + u * T::kXRaw + 1024 + lane * 4);
+        const float s = FMT == MOEDISP_SCALE_FP32 ? __int_as_float(xs) : ue8m0_value((uint32_t)xs);
+        const uint32_t on = step * kStep + x_row < rows ? 0xFFFFFFFFu : 0u;
         v4u o[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[u][i], false);
-            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[u][i], true);
-            o[i >> 1][2 * (i & 1)] = on ? pack_bf16x2(lo.x * s, lo.y * s) : 0u;
-            o[i >> 1][2 * (i & 1) + 1] = on ? pack_bf16x2(hi.x * s, hi.y * s) : 0u;
+            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], false);
+            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], true);
+            o[i >> 1][2 * (i & 1)] = pack_bf16x2(lo.x * s, lo.y * s) & on;
+            o[i >> 1][2 * (i & 1) + 1] = pack_bf16x2(hi.x * s, hi.y * s) & on;
         }
         char* to = x_lds + (step & 1) * T::kXStage + x_at;
         *reinterpret_cast<v4u*>(to + x_half * 16) = x_half ? o[1] : o[0];
@@ -150,11 +183,11 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
 
     if (steps > 0) {
 #pragma unroll
-        for (int p = 0; p < kStages; ++p) {
+        for (int p = 0; p < kStages - 1; ++p) {
             load_x(p, p);
-            if (p < kStages - 1) load_dy(p, p);
-            __builtin_amdgcn_sched_barrier(0);
+            load_dy(p, p);
         }
+        wait_own_loads<(kStages - 2) * T::kOps>();
         stage_x(0, 0);
         wait_loads_and_sync<(kStages - 2) * T::kOps>();
         for (int s0 = 0; s0 < steps; s0 += kStages) {
@@ -162,10 +195,6 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
             for (int h = 0; h < kStages; ++h) {
                 const int s = s0 + h;
                 if (s >= steps) break;
-                load_x(s + kStages, h);
-                load_dy(s + kStages - 1, (h + kStages - 1) % kStages);
-                __builtin_amdgcn_sched_barrier(0);
-                stage_x(s + 1, (h + 1) % kStages);
                 const char* ds = lds + h * T::kDyStage;
                 const char* xst = x_lds + (h & 1) * T::kXStage;
                 v8bf b[T::kNT], av[2];
@@ -179,6 +208,15 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
                     for (int j = 0; j < T::kNT; ++j)
                         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1], b[j], acc[i][j], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
+                    // behind the products: step s + 3 into the place of step
+                    // s - 1, which all waves have read; x of step s + 1
+                    if (i == 0) load_x(s + kStages - 1, (h + kStages - 1) % kStages);
+                    if (i == 1) load_dy(s + kStages - 1, (h + kStages - 1) % kStages);
+                    if (i == 2) {
+                        wait_own_loads<(kStages - 2) * T::kOps>();
+                        stage_x(s + 1, (h + 1) % kStages);
+                    }
+                    if (i < 3) __builtin_amdgcn_sched_barrier(0);
                 }
                 wait_loads_and_sync<(kStages - 2) * T::kOps>();
             }
@@ -220,13 +258,21 @@ hipError_t launch_one(ExpertWgradArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-#ifndef WTILE
-#define WTILE 256, 256, 4, 2
-#endif
+// Tiles of 256 x 256 move the fewest bytes per product; where they would not
+// give every compute unit one, tiles of 128 x 128 (two workgroups to a unit):
+// 8 experts of 512 x 512 and 1024 rows 24 us against 47, but 8 of 1024 x 2048
+// (256 large tiles) 49 us large against 64 small.
+template <int FMT, bool F32, bool ADD>
+hipError_t launch_tiles(const ExpertWgradArgs& a, hipStream_t stream) {
+    const long long large = (long long)a.r.E * ((a.n + 255) / 256) * ((a.k + 255) / 256);
+    return large >= 256 ? launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream)
+                        : launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
+}
+
 template <int FMT>
 hipError_t launch_fmt(const ExpertWgradArgs& a, bool f32_out, bool accumulate, hipStream_t stream) {
-    if (!f32_out) return launch_one<WTILE, FMT, false, false>(a, stream);
-    return accumulate ? launch_one<WTILE, FMT, true, true>(a, stream) : launch_one<WTILE, FMT, true, false>(a, stream);
+    if (!f32_out) return launch_tiles<FMT, false, false>(a, stream);
+    return accumulate ? launch_tiles<FMT, true, true>(a, stream) : launch_tiles<FMT, true, false>(a, stream);
 }
 
 }  // namespace
