@@ -37,10 +37,25 @@ __device__ inline bool row_used(const RowsArg& r, int row) {
     return i >= 0 && i < min(r.bounds[e], r.cap);
 }
 
-__device__ inline float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// s = 1 / (1 + exp(-v)), good to about one step.  exp(-v) = 2^h (1 + l ln 2)
+// with h + l = -v / ln 2 to twice the bits of binary32; the quotient is
+// v_rcp_f32 with one correction.  The rows' memory traffic leaves room for
+// about 30 instructions per value: expf and a division are 27 of their own.
+// Beyond +-87, where 2^h would leave the normal range, s is 0 or 1 (for NaN
+// any: its factor v is NaN).
+__device__ inline float sigmoid(float v) {
+    const float x = __builtin_amdgcn_fmed3f(v, -87.0f, 87.0f);
+    const float h = x * -0x1.715476p+0f;
+    float l = __builtin_fmaf(x, -0x1.715476p+0f, -h);
+    l = __builtin_fmaf(x, -0x1.4ae0c0p-26f, l);
+    const float p = __builtin_amdgcn_exp2f(h);
+    const float d = 1.0f + __builtin_fmaf(p, l * 0x1.62e430p-1f, p);
+    const float r = __builtin_amdgcn_rcpf(d);
+    const float s = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+    return v < -87.0f ? 0.0f : s;
+}
 
-__device__ inline void unpack8(const uint16_t* p, float f[8]) {
-    const v4u v = *reinterpret_cast<const v4u*>(p);
+__device__ inline void unpack8(v4u v, float f[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f[2 * i] = bf16_low(v[i]);
@@ -53,7 +68,8 @@ template <int FMT>
 __device__ inline void quantise(const float f[8], uint8_t* q, void* scales, size_t at, bool lead) {
     uint32_t top = 0;  // magnitudes compare as integers; NaN and infinity are the largest
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; i += 2)
+        top = max(max(__float_as_uint(f[i]) & 0x7FFFFFFFu, __float_as_uint(f[i + 1]) & 0x7FFFFFFFu), top);
 #pragma unroll
     for (int m = 1; m < 16; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
     const bool finite = top < 0x7F800000u;
@@ -63,10 +79,19 @@ __device__ inline void quantise(const float f[8], uint8_t* q, void* scales, size
     int sx = 0;
     if (FMT == MOEDISP_SCALE_FP32) {
         scale = amax > 0.0f ? amax / 448.0f : 1.0f;
-        out.x = (int)pack4_e4m3(clamp448(f[0] / scale), clamp448(f[1] / scale), clamp448(f[2] / scale),
-                                clamp448(f[3] / scale));
-        out.y = (int)pack4_e4m3(clamp448(f[4] / scale), clamp448(f[5] / scale), clamp448(f[6] / scale),
-                                clamp448(f[7] / scale));
+        // The quotient by the reciprocal: two roundings, which exceed 448 by
+        // so little that E4M3 rounds it to 448.  A scale whose reciprocal
+        // overflows (below 2^-127) takes the division.
+        const float inv = 1.0f / scale;
+        if (inv < INFINITY) {
+            out.x = (int)pack4_e4m3(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+            out.y = (int)pack4_e4m3(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+        } else {
+            out.x = (int)pack4_e4m3(clamp448(f[0] / scale), clamp448(f[1] / scale), clamp448(f[2] / scale),
+                                    clamp448(f[3] / scale));
+            out.y = (int)pack4_e4m3(clamp448(f[4] / scale), clamp448(f[5] / scale), clamp448(f[6] / scale),
+                                    clamp448(f[7] / scale));
+        }
     } else {
         sx = ue8m0_exponent(amax);
         out.x = (int)pack4_e4m3(clamp448(ldexpf(f[0], -sx)), clamp448(ldexpf(f[1], -sx)), clamp448(ldexpf(f[2], -sx)),
@@ -85,7 +110,7 @@ __device__ inline void quantise(const float f[8], uint8_t* q, void* scales, size
 }
 
 template <int FMT, bool BACKWARD>
-__global__ __launch_bounds__(kSwigluThreads) void moedisp_swiglu(SwigluArgs a) {
+__global__ __launch_bounds__(kSwigluThreads, BACKWARD ? 7 : 8) void moedisp_swiglu(SwigluArgs a) {
     int first, end;
     if (!check_bounds(a.r, &first, &end)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&a.hdr->status, (uint32_t)MOEDISP_DEV_BAD_LAYOUT);
@@ -105,15 +130,20 @@ __global__ __launch_bounds__(kSwigluThreads) void moedisp_swiglu(SwigluArgs a) {
         for (int b = b0; b < a.blocks; b += kUnits) {
             const int c = b * kScaleBlock + l * 8;
             float g[8], u[8], o[8];
-            unpack8(a.gu + (size_t)row * 2 * a.inner + c, g);
-            unpack8(a.gu + (size_t)row * 2 * a.inner + a.inner + c, u);
+            const v4u gv = *reinterpret_cast<const v4u*>(a.gu + (size_t)row * 2 * a.inner + c);
+            const v4u uv = *reinterpret_cast<const v4u*>(a.gu + (size_t)row * 2 * a.inner + a.inner + c);
+            v4u dv = {0u, 0u, 0u, 0u};
+            if (BACKWARD) dv = *reinterpret_cast<const v4u*>(a.dh + (size_t)row * a.inner + c);
+            __builtin_amdgcn_sched_barrier(0);  // all loads before the first use
+            unpack8(gv, g);
+            unpack8(uv, u);
             if (!BACKWARD) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
                 quantise<FMT>(o, a.q + (size_t)row * a.inner + c, a.q_scales, (size_t)row * a.blocks + b, l == 0);
             } else {
                 float d[8], o2[8];
-                unpack8(a.dh + (size_t)row * a.inner + c, d);
+                unpack8(dv, d);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float s = sigmoid(g[i]);
@@ -143,7 +173,7 @@ template <bool BACKWARD>
 hipError_t launch(const SwigluArgs& a, int scale_fmt, hipStream_t stream) {
     const long long rows_at_once = a.blocks >= kUnits ? 1 : kUnits / a.blocks;
     long long blocks = ((long long)a.r.max_rows + rows_at_once - 1) / rows_at_once;
-    if (blocks > 256 * 8) blocks = 256 * 8;  // resident workgroups of the device
+    if (blocks > 256 * (BACKWARD ? 7 : 8)) blocks = 256 * (BACKWARD ? 7 : 8);  // all resident at once
     if (blocks < 1) blocks = 1;              // the bounds are checked even where no row can be
     if (scale_fmt == MOEDISP_SCALE_UE8M0)
         hipLaunchKernelGGL((moedisp_swiglu<MOEDISP_SCALE_UE8M0, BACKWARD>), dim3((unsigned)blocks),

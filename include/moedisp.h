@@ -436,8 +436,9 @@ int ep_expert_wgrad(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scal
 
 /* Gated activation with quantisation, between the two products of an expert:
  *   h[i] = silu(g[i]) * u[i] for gu's row (g[0..inner), u[0..inner)),
- *   silu(v) = v / (1 + exp(-v)), computed in binary32 and quantised per block
- * of 128 by the rules of ep_dispatch_quant (scale_fmt FP32 or UE8M0).
+ *   silu(v) = v / (1 + exp(-v)), computed in binary32 (zero for v < -87) and
+ * quantised per block of 128 as ep_dispatch_quant does (scale_fmt FP32 or
+ * UE8M0; the quotient h / scale is good to two steps of binary32).
  *   inner     inner % 128 == 0, in [128, 65536].
  *   gu        bf16 [max_rows][2*inner];  h E4M3 [max_rows][inner];
  *   h_scales  [max_rows][inner/128] float or uint8.
