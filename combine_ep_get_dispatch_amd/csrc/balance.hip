@@ -14,120 +14,242 @@ namespace moedisp {
 namespace {
 
 constexpr int kBalThreads = 256;
+constexpr int kSeqThreads = 1024;
+constexpr int kSeqCols = 64;  // experts of a workgroup that sums tiles
 
-template <bool BF16>
-__device__ inline float load_logit(const void* p, size_t i) {
-    if (BF16) return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << 16);
-    return reinterpret_cast<const float*>(p)[i];
+template <int CTRL>
+__device__ inline float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 
-// Sum (or largest) over a row's LPR lanes; every lane gets it.
+// op over a row's LPR lanes (aligned), every lane gets it: exchanges by
+// register moves, no LDS.  After steps 1 and 2 the lanes of 4 agree, so
+// mirroring 8 and then 16 lanes meets the other half.
+template <int LPR, class OP>
+__device__ inline float row_reduce(float v, OP op) {
+    if (LPR > 1) v = op(v, dpp<0xB1>(v));
+    if (LPR > 2) v = op(v, dpp<0x4E>(v));
+    if (LPR > 4) v = op(v, dpp<0x141>(v));
+    if (LPR > 8) v = op(v, dpp<0x140>(v));
+    if (LPR > 16) {  // both 16-lane rows' values, in the same order for both
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    if (LPR > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    return v;
+}
 template <int LPR>
 __device__ inline float lanes_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    return row_reduce<LPR>(v, [](float x, float y) { return x + y; });
 }
 template <int LPR>
 __device__ inline float lanes_max(float v) {
-#pragma unroll
-    for (int m = 1; m < LPR; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-    return v;
+    return row_reduce<LPR>(v, [](float x, float y) { return fmaxf(x, y); });
 }
 
-// Scores p and their slopes (1 for softmax, 1 - s(z) for sigmoid) of one row;
-// lane l of the row's LPR lanes holds experts l, l + LPR, ...
-template <int LPR, int VPL, bool BF16>
-__device__ inline void row_scores(const BalanceArgs& a, size_t row, int l, float p[VPL], float slope[VPL]) {
-    float z[VPL];
+// Whether any of the row's LPR lanes has it.
+template <int LPR>
+__device__ inline bool lanes_any(bool v) {
+    const uint64_t b = __ballot(v);
+    if (LPR == 64) return b != 0;
+    const int at = (threadIdx.x & 63) / LPR * LPR;
+    return ((b >> at) & ((1ull << (LPR & 63)) - 1ull)) != 0;
+}
+
+// The row's logits as they are stored: lane l of its LPR lanes holds experts
+// (c * LPR + l) * 8 .. + 7 of chunk c; one or two 16-byte loads a chunk where
+// rows are whole multiples of 8 experts (VEC).
+template <int LPR, int CH, bool BF16, bool VEC>
+struct Row {
+    v4u raw[VEC ? CH * (BF16 ? 1 : 2) : 1];
+    float one[VEC ? 1 : CH * 8];
+
+    // -inf everywhere: lanes past the last expert keep it (VEC)
+    __device__ inline void clear() {
+        const uint32_t v = BF16 ? 0xFF80FF80u : 0xFF800000u;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        const int e = v * LPR + l;
-        z[v] = e < a.E ? load_logit<BF16>(a.logits, row * a.E + e) : -INFINITY;
+        for (int i = 0; i < (VEC ? CH * (BF16 ? 1 : 2) : 1); ++i) raw[i] = v4u{v, v, v, v};
     }
+
+    __device__ inline void load(const BalanceArgs& a, size_t row, int l) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int e0 = (c * LPR + l) * 8;
+            if (VEC) {
+                const size_t at = row * a.E + e0;
+                if (e0 >= a.E) continue;
+                if (BF16) {
+                    raw[c] = *reinterpret_cast<const v4u*>(reinterpret_cast<const uint16_t*>(a.logits) + at);
+                } else {
+                    const v4u* p = reinterpret_cast<const v4u*>(reinterpret_cast<const float*>(a.logits) + at);
+                    raw[2 * c] = p[0];
+                    raw[2 * c + 1] = p[1];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const size_t at = row * a.E + (e0 + i < a.E ? e0 + i : 0);
+                    one[c * 8 + i] =
+                        BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.logits)[at] << 16)
+                             : reinterpret_cast<const float*>(a.logits)[at];
+                }
+            }
+        }
+    }
+    __device__ inline void values(const BalanceArgs& a, int l, float z[CH * 8]) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float& v = z[c * 8 + i];
+                if (!VEC)
+                    v = (c * LPR + l) * 8 + i < a.E ? one[c * 8 + i] : -INFINITY;
+                else if (BF16)
+                    v = (i & 1) ? bf16_high(raw[c][i >> 1]) : bf16_low(raw[c][i >> 1]);
+                else
+                    v = __uint_as_float(raw[2 * c + (i >> 2)][i & 3]);
+            }
+    }
+};
+
+__device__ inline float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f); }
+
+// Scores of one row times a common factor, and the factor's inverse: score v
+// is p[v] * the result.  For the sigmoid also the slopes 1 - s(z) if wanted.
+template <int LPR, int N, bool SLOPE>
+__device__ inline float row_scores(bool sigmoid, const float z[N], float p[N], float slope[N]) {
     float sum = 0.0f, m = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) m = fmaxf(m, z[v]);
+    for (int v = 0; v < N; ++v) m = fmaxf(m, z[v]);
     m = lanes_max<LPR>(m);
-    if (a.sigmoid) {
-        // a common factor cancels: where every logit is negative the scores
-        // are taken times exp(-m), so that they do not vanish together
-        m = fminf(m, 0.0f);
+    if (sigmoid) {
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            const float x = expf(-fabsf(z[v]));
-            const float inv = 1.0f / (1.0f + x);
-            slope[v] = z[v] >= 0.0f ? x * inv : inv;
-            p[v] = z[v] >= 0.0f ? inv : z[v] == -INFINITY ? 0.0f : expf(z[v] - m) * inv;
-            sum += p[v];
+        for (int v = 0; v < N; ++v) {
+            const float x = exp_of(-z[v]);
+            p[v] = __builtin_amdgcn_rcpf(1.0f + x);
+            if (SLOPE) slope[v] = z[v] >= 0.0f ? x * p[v] : 1.0f - p[v];
+        }
+        // Where every logit is far below zero s(z) is exp(z) (1 - s(z)): the
+        // factor exp(-m) keeps the scores from vanishing together.
+        if (__any(m < -8.0f)) {
+#pragma unroll
+            for (int v = 0; v < N; ++v)
+                if (m < -8.0f) p[v] = z[v] == -INFINITY ? 0.0f : exp_of(z[v] - m) * (1.0f - p[v]);
         }
     } else {
+        m = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            p[v] = z[v] == -INFINITY ? 0.0f : expf(z[v] - m);
-            slope[v] = 1.0f;
-            sum += p[v];
-        }
+        for (int v = 0; v < N; ++v) p[v] = exp_of(z[v] - m);
     }
-    sum = lanes_sum<LPR>(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no score at all: p = 0
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) p[v] *= inv;
+    for (int v = 0; v < N; ++v) sum += p[v];
+    sum = lanes_sum<LPR>(sum);
+    return sum == 0.0f ? 0.0f : 1.0f / sum;  // no score at all: 0
+}
+
+// Slot l of the row (loaded with the row's logits, a row ahead), masked where
+// there is none.
+__device__ inline int first_slot(const BalanceArgs& a, size_t row, int l) {
+    return l < a.k ? a.topk_idx[row * a.k + l] : -1;
+}
+
+// Whether the row has a routed slot, counted per expert if `count` is given.
+// `id` is the lane's first_slot.
+template <int LPR>
+__device__ inline bool row_routed(const BalanceArgs& a, size_t row, int l, bool valid, int id, int* count, bool* bad) {
+    bool routed = false;
+    if (valid)
+        for (int j = l; j < a.k; j += LPR) {
+            if (j != l) id = a.topk_idx[row * a.k + j];
+            if (id >= 0 && id < a.E) {
+                if (count) atomicAdd(&count[id], 1);
+                routed = true;
+            } else if (id != -1) {
+                *bad = true;
+            }
+        }
+    return lanes_any<LPR>(routed);
 }
 
 // Forward, first launch: the score sums [E], slot counts [E] and token count
-// of one tile.
-template <int LPR, int VPL, bool BF16>
+// of one tile.  A row's lanes keep the sums of their experts over the tile's
+// rows; the next row is loaded before the present one is worked on.
+template <int LPR, int CH, bool BF16, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void moedisp_balance_tile(BalanceArgs a) {
     constexpr int kRows = kBalThreads / LPR;  // rows at a time
+    constexpr int N = CH * 8;
     extern __shared__ float s_p[];            // [kRows][E], then int [E], int
     int* s_c = reinterpret_cast<int*>(s_p + kRows * a.E);
     int* s_n = s_c + a.E;
     const int tid = threadIdx.x;
     const int seq = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
     const int t0 = tile * a.tile_tokens, t1 = min(a.L, t0 + a.tile_tokens);
+    const int l = tid % LPR, r = tid / LPR;
+    const size_t row0 = (size_t)seq * a.L;
+    Row<LPR, CH, BF16, VEC> cur;
+    cur.clear();
+    cur.load(a, row0 + min(t0 + r, t1 - 1), l);
+    int id = first_slot(a, row0 + min(t0 + r, t1 - 1), l);
     for (int e = tid; e < a.E + 1; e += kBalThreads) s_c[e] = 0;
     __syncthreads();
-    const int l = tid % LPR, r = tid / LPR;
-    float acc[VPL];
+    float acc[N];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) acc[v] = 0.0f;
+    for (int v = 0; v < N; ++v) acc[v] = 0.0f;
     bool bad = false;
-    for (int t = t0 + r; t < t1; t += kRows) {
-        const size_t row = (size_t)seq * a.L + t;
-        int routed = 0;
-        for (int j = l; j < a.k; j += LPR) {
-            const int id = a.topk_idx[row * a.k + j];
-            if (id >= 0 && id < a.E) {
-                atomicAdd(&s_c[id], 1);
-                routed = 1;
-            } else if (id != -1) {
-                bad = true;
-            }
+    int n = 0;
+    for (int base = t0; base < t1; base += kRows) {
+        const int t = base + r;
+        const bool valid = t < t1;
+        Row<LPR, CH, BF16, VEC> next = cur;
+        if (CH == 1 && base + kRows < t1) next.load(a, row0 + min(t + kRows, t1 - 1), l);
+        const int next_id = base + kRows < t1 ? first_slot(a, row0 + min(t + kRows, t1 - 1), l) : -1;
+        const bool routed = row_routed<LPR>(a, row0 + t, l, valid, id, s_c, &bad);
+        float z[N], p[N], slope[N];
+        cur.values(a, l, z);
+        const float inv = row_scores<LPR, N, false>(a.sigmoid, z, p, slope);
+        if (routed) {
+            ++n;
+#pragma unroll
+            for (int v = 0; v < N; ++v) acc[v] = __builtin_fmaf(p[v], inv, acc[v]);
         }
-#pragma unroll
-        for (int m = 1; m < LPR; m <<= 1) routed |= __shfl_xor(routed, m);
-        if (!routed) continue;  // all of the row's lanes
-        if (l == 0) atomicAdd(s_n, 1);
-        float p[VPL], slope[VPL];
-        row_scores<LPR, VPL, BF16>(a, row, l, p, slope);
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) acc[v] += p[v];
+        id = next_id;
+        if (CH == 1)
+            cur = next;
+        else if (base + kRows < t1)
+            cur.load(a, row0 + min(t + kRows, t1 - 1), l);
     }
+    if (l == 0 && n) atomicAdd(s_n, n);
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-        if (v * LPR + l < a.E) s_p[r * a.E + v * LPR + l] = acc[v];
+    for (int v = 0; v < N; ++v) {
+        const int e = ((v >> 3) * LPR + l) * 8 + (v & 7);
+        if (e < a.E) s_p[r * a.E + e] = acc[v];
+    }
     if (bad) atomicOr(&a.hdr->status, (uint32_t)MOEDISP_DEV_BAD_EXPERT_ID);
     __syncthreads();
+    // the rows' sums: first every parts-th row (parts * E lanes, each into the
+    // row that only it reads), then those
+    const int parts = min(kRows, max(1, kBalThreads / a.E));
+    if (parts > 1) {
+        if (tid < parts * a.E) {
+            float sum = 0.0f;
+            for (int i = tid / a.E; i < kRows; i += parts) sum += s_p[i * a.E + tid % a.E];
+            s_p[tid] = sum;
+        }
+        __syncthreads();
+    }
     for (int e = tid; e < a.E; e += kBalThreads) {
         float sum = 0.0f;
-        for (int i = 0; i < kRows; ++i) sum += s_p[i * a.E + e];
+        for (int i = 0; i < (parts > 1 ? parts : kRows); ++i) sum += s_p[i * a.E + e];
         a.psum[(size_t)blockIdx.x * a.E + e] = sum;
         a.count[(size_t)blockIdx.x * a.E + e] = s_c[e];
     }
     if (tid == 0) a.tokens[blockIdx.x] = *s_n;
 }
 
+// Sum over the workgroup in a fixed order, for every lane.
 __device__ inline double block_sum(double v, double* s) {
     for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
     __syncthreads();
@@ -138,141 +260,227 @@ __device__ inline double block_sum(double v, double* s) {
     return t;
 }
 
-// Forward, second launch: one workgroup per sequence sums its tiles.
-__global__ __launch_bounds__(1024) void moedisp_balance_seq(BalanceArgs a) {
-    __shared__ double s_sum[16];
-    const int seq = blockIdx.x, tid = threadIdx.x;
-    long long n = 0;
-    for (int t = 0; t < a.tiles; ++t) n += a.tokens[(size_t)seq * a.tiles + t];
-    double part = 0.0;
-    for (int e = tid; e < a.E; e += blockDim.x) {
-        double p = 0.0;
+// Forward, second launch: a workgroup sums the tiles of 64 experts of one
+// sequence (its 16 waves every 16th tile, joined in order) and their part of
+// the loss; the last workgroup to finish adds the parts up in order.
+__global__ __launch_bounds__(kSeqThreads) void moedisp_balance_seq(BalanceArgs a) {
+    constexpr int kW = kSeqThreads / 64;
+    __shared__ double s_sum[kW];
+    __shared__ float s_p[kW][kSeqCols];
+    __shared__ int s_c[kW][kSeqCols];
+    __shared__ int s_n[kW];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int cols = (a.E + kSeqCols - 1) / kSeqCols;
+    if (a.S > 0) {
+        const int seq = blockIdx.x / cols, e = blockIdx.x % cols * kSeqCols + lane;
+        float p = 0.0f;
         int c = 0;
-        for (int t = 0; t < a.tiles; ++t) {
-            const size_t at = ((size_t)seq * a.tiles + t) * a.E + e;
-            p += a.psum[at];
-            c += a.count[at];
+        if (e < a.E) {
+            const size_t at = (size_t)seq * a.tiles * a.E + e;
+#pragma unroll 4
+            for (int t = wave; t < a.tiles; t += kW) {
+                p += a.psum[at + (size_t)t * a.E];
+                c += a.count[at + (size_t)t * a.E];
+            }
         }
-        a.tokens_per_expert[(size_t)seq * a.E + e] = c;
-        part += p * c;
+        s_p[wave][lane] = p;
+        s_c[wave][lane] = c;
+        int tok = 0;
+        for (int t = tid; t < a.tiles; t += kSeqThreads) tok += a.tokens[(size_t)seq * a.tiles + t];
+        tok = wave_sum_dpp(tok);
+        if (lane == 0) s_n[wave] = tok;
+        __syncthreads();
+        double n = 0.0;
+        for (int w = 0; w < kW; ++w) n += s_n[w];
+        if (wave == 0) {
+            double pt = 0.0;
+            int ct = 0;
+            for (int w = 0; w < kW; ++w) {
+                pt += s_p[w][lane];
+                ct += s_c[w][lane];
+            }
+            if (e < a.E) a.tokens_per_expert[(size_t)seq * a.E + e] = ct;
+            double part = pt * ct;
+            for (int m = 1; m < 64; m <<= 1) part += __shfl_xor(part, m);
+            if (lane == 0) {
+                if (blockIdx.x % cols == 0) a.tokens_per_seq[seq] = (int)n;
+                part = n > 0.0 ? part * a.E / ((double)a.k * n * n) : 0.0;
+                __hip_atomic_store(a.part + blockIdx.x, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                if (blockIdx.x % cols == 0)
+                    __hip_atomic_store(a.some + seq, n > 0.0 ? 1 : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
     }
-    const double sum = block_sum(part, s_sum);
     if (tid == 0) {
-        a.tokens_per_seq[seq] = (int)n;
-        a.seq_loss[seq] = n > 0 ? (float)(sum * a.E / ((double)a.k * n * n)) : 0.0f;
+        // The parts above are stored past the caches of the XCD and read past
+        // them below; they have arrived before the counter goes up.  (Release
+        // and acquire order would write back and drop a whole L2: 4 us.)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t before =
+            __hip_atomic_fetch_add(&a.hdr->reserved0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = before == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    double sum = 0.0, some = 0.0;
+    for (int i = tid; i < a.S * cols; i += kSeqThreads)
+        sum += __hip_atomic_load(a.part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = tid; i < a.S; i += kSeqThreads)
+        some += __hip_atomic_load(a.some + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sum = block_sum(sum, s_sum);
+    some = block_sum(some, s_sum);
+    if (tid == 0) {
+        *a.loss = some > 0.0 ? (float)(a.coef * sum / some) : 0.0f;
+        __hip_atomic_store(&a.hdr->reserved0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
     }
 }
 
-// Forward, third launch: the mean over the sequences.
-__global__ __launch_bounds__(256) void moedisp_balance_loss(BalanceArgs a) {
-    __shared__ double s_sum[4];
-    double part = 0.0, some = 0.0;
-    for (int s = threadIdx.x; s < a.S; s += blockDim.x) {
-        part += a.seq_loss[s];
-        some += a.tokens_per_seq[s] > 0 ? 1.0 : 0.0;
-    }
-    const double sum = block_sum(part, s_sum);
-    const double n = block_sum(some, s_sum);
-    if (threadIdx.x == 0) *a.loss = n > 0.0 ? (float)(a.coef * sum / n) : 0.0f;
-}
-
-// Backward.
-template <int LPR, int VPL, bool BF16>
+// Backward: one pass over the rows as in the forward's first launch.
+template <int LPR, int CH, bool BF16, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void moedisp_balance_backward(BalanceArgs a) {
     constexpr int kRows = kBalThreads / LPR;
-    __shared__ double s_sum[4];
+    constexpr int N = CH * 8;
     const int tid = threadIdx.x;
     const int seq = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
     const int t0 = tile * a.tile_tokens, t1 = min(a.L, t0 + a.tile_tokens);
-    double some = 0.0;
-    for (int s = tid; s < a.S; s += kBalThreads) some += a.tokens_per_seq[s] > 0 ? 1.0 : 0.0;
-    some = block_sum(some, s_sum);
-    const double n = a.tokens_per_seq[seq];
-    const float scale = n > 0.0 ? (float)((double)a.coef * a.E * *a.d_loss / (some * a.k * n * n)) : 0.0f;
     const int l = tid % LPR, r = tid / LPR;
-    float w[VPL];
+    const size_t row0 = (size_t)seq * a.L;
+    Row<LPR, CH, BF16, VEC> cur;
+    cur.clear();
+    cur.load(a, row0 + min(t0 + r, t1 - 1), l);
+    int id = first_slot(a, row0 + min(t0 + r, t1 - 1), l);
+    int some = 0;
+    for (int s = tid; s < a.S; s += kBalThreads) some += a.tokens_per_seq[s] > 0 ? 1 : 0;
+    for (int m = 1; m < 64; m <<= 1) some += __shfl_xor(some, m);
+    __shared__ int s_some[kBalThreads / 64];
+    if ((tid & 63) == 0) s_some[tid >> 6] = some;
+    __syncthreads();
+    some = s_some[0] + s_some[1] + s_some[2] + s_some[3];
+    const double n = a.tokens_per_seq[seq];
+    const float scale = n > 0.0 ? (float)((double)a.coef * a.E * *a.d_loss / ((double)some * a.k * n * n)) : 0.0f;
+    float w[N];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        const int e = v * LPR + l;
+    for (int v = 0; v < N; ++v) {
+        const int e = ((v >> 3) * LPR + l) * 8 + (v & 7);
         w[v] = e < a.E ? scale * (float)a.tokens_per_expert[(size_t)seq * a.E + e] : 0.0f;
     }
-    for (int t = t0 + r; t < t1; t += kRows) {
-        const size_t row = (size_t)seq * a.L + t;
-        int routed = 0;
-        for (int j = l; j < a.k; j += LPR) {
-            const int id = a.topk_idx[row * a.k + j];
-            routed |= id >= 0 && id < a.E;
-        }
-#pragma unroll
-        for (int m = 1; m < LPR; m <<= 1) routed |= __shfl_xor(routed, m);
-        float p[VPL], slope[VPL];
+    bool bad = false;
+    for (int base = t0; base < t1; base += kRows) {
+        const int t = base + r;
+        const bool valid = t < t1;
+        Row<LPR, CH, BF16, VEC> next = cur;
+        if (CH == 1 && base + kRows < t1) next.load(a, row0 + min(t + kRows, t1 - 1), l);
+        const int next_id = base + kRows < t1 ? first_slot(a, row0 + min(t + kRows, t1 - 1), l) : -1;
+        const bool routed = row_routed<LPR>(a, row0 + t, l, valid, id, nullptr, &bad);
+        float z[N], p[N], slope[N];
+        cur.values(a, l, z);
+        const float inv = row_scores<LPR, N, true>(a.sigmoid, z, p, slope);
         float dot = 0.0f;
-        if (routed) {
-            row_scores<LPR, VPL, BF16>(a, row, l, p, slope);
 #pragma unroll
-            for (int v = 0; v < VPL; ++v) dot += p[v] * w[v];
-            dot = lanes_sum<LPR>(dot);
+        for (int v = 0; v < N; ++v) {
+            p[v] *= inv;
+            dot = __builtin_fmaf(p[v], w[v], dot);
+        }
+        dot = lanes_sum<LPR>(dot);
+#pragma unroll
+        for (int v = 0; v < N; ++v) {
+            const float dz = p[v] * (w[v] - dot);
+            z[v] = a.sigmoid ? dz * slope[v] : dz;
+        }
+        if (!routed) {
+#pragma unroll
+            for (int v = 0; v < N; ++v) z[v] = 0.0f;
         }
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) {
-            const int e = v * LPR + l;
-            if (e >= a.E) continue;
-            const float dz = routed ? p[v] * slope[v] * (w[v] - dot) : 0.0f;
-            if (BF16)
-                reinterpret_cast<uint16_t*>(a.d_logits)[row * a.E + e] = (uint16_t)pack_bf16x2(dz, 0.0f);
-            else
-                reinterpret_cast<float*>(a.d_logits)[row * a.E + e] = dz;
+        for (int c = 0; c < CH; ++c) {
+            const int e0 = (c * LPR + l) * 8;
+            const size_t at = (row0 + t) * a.E + e0;
+            const float* d = z + c * 8;
+            if (VEC) {
+                if (valid && e0 < a.E) {
+                    if (BF16) {
+                        const v4u o = {pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
+                                       pack_bf16x2(d[6], d[7])};
+                        *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.d_logits) + at) = o;
+                    } else {
+                        v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.d_logits) + at);
+                        o[0] = v4f{d[0], d[1], d[2], d[3]};
+                        o[1] = v4f{d[4], d[5], d[6], d[7]};
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (valid && e0 + i < a.E) {
+                        if (BF16)
+                            reinterpret_cast<uint16_t*>(a.d_logits)[at + i] = (uint16_t)pack_bf16x2(d[i], 0.0f);
+                        else
+                            reinterpret_cast<float*>(a.d_logits)[at + i] = d[i];
+                    }
+            }
         }
+        id = next_id;
+        if (CH == 1)
+            cur = next;
+        else if (base + kRows < t1)
+            cur.load(a, row0 + min(t + kRows, t1 - 1), l);
     }
 }
 
-template <int LPR, int VPL, bool BF16>
+template <int LPR, int CH, bool BF16, bool VEC>
 hipError_t launch_pass(const BalanceArgs& a, bool backward, hipStream_t stream) {
     const long long blocks = (long long)a.S * a.tiles;
     if (!grid_fits(blocks, kBalThreads)) return hipErrorInvalidConfiguration;
     if (backward) {
-        hipLaunchKernelGGL((moedisp_balance_backward<LPR, VPL, BF16>), dim3((unsigned)blocks), dim3(kBalThreads), 0,
-                           stream, a);
+        hipLaunchKernelGGL((moedisp_balance_backward<LPR, CH, BF16, VEC>), dim3((unsigned)blocks), dim3(kBalThreads),
+                           0, stream, a);
     } else {
         const size_t lds = ((size_t)(kBalThreads / LPR) * a.E + a.E + 1) * 4;
-        hipLaunchKernelGGL((moedisp_balance_tile<LPR, VPL, BF16>), dim3((unsigned)blocks), dim3(kBalThreads), lds,
+        hipLaunchKernelGGL((moedisp_balance_tile<LPR, CH, BF16, VEC>), dim3((unsigned)blocks), dim3(kBalThreads), lds,
                            stream, a);
     }
     return hipGetLastError();
 }
 
-// Lanes per row: at most 4 experts a lane up to 256 experts, a wave per row
-// beyond.
-template <bool BF16>
+template <bool BF16, bool VEC>
 hipError_t launch_rows(const BalanceArgs& a, bool backward, hipStream_t stream) {
-    if (a.E <= 8) return launch_pass<2, 4, BF16>(a, backward, stream);
-    if (a.E <= 16) return launch_pass<4, 4, BF16>(a, backward, stream);
-    if (a.E <= 32) return launch_pass<8, 4, BF16>(a, backward, stream);
-    if (a.E <= 64) return launch_pass<16, 4, BF16>(a, backward, stream);
-    if (a.E <= 128) return launch_pass<32, 4, BF16>(a, backward, stream);
-    if (a.E <= 256) return launch_pass<64, 4, BF16>(a, backward, stream);
-    if (a.E <= 512) return launch_pass<64, 8, BF16>(a, backward, stream);
-    if (a.E <= 1024) return launch_pass<64, 16, BF16>(a, backward, stream);
-    return launch_pass<64, 64, BF16>(a, backward, stream);
+    switch (balance_lanes(a.E)) {
+        case 1: return launch_pass<1, 1, BF16, VEC>(a, backward, stream);
+        case 2: return launch_pass<2, 1, BF16, VEC>(a, backward, stream);
+        case 4: return launch_pass<4, 1, BF16, VEC>(a, backward, stream);
+        case 8: return launch_pass<8, 1, BF16, VEC>(a, backward, stream);
+        case 16: return launch_pass<16, 1, BF16, VEC>(a, backward, stream);
+        case 32: return launch_pass<32, 1, BF16, VEC>(a, backward, stream);
+        default: break;
+    }
+    if (a.E <= 512) return launch_pass<64, 1, BF16, VEC>(a, backward, stream);
+    if (a.E <= 1024) return launch_pass<64, 2, BF16, VEC>(a, backward, stream);
+    return launch_pass<64, 8, BF16, VEC>(a, backward, stream);
+}
+
+hipError_t launch_type(const BalanceArgs& a, bool bf16, bool backward, hipStream_t stream) {
+    const bool vec = a.E % 8 == 0;
+    if (bf16) return vec ? launch_rows<true, true>(a, backward, stream) : launch_rows<true, false>(a, backward, stream);
+    return vec ? launch_rows<false, true>(a, backward, stream) : launch_rows<false, false>(a, backward, stream);
 }
 
 }  // namespace
 
 hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t stream) {
-    hipError_t e = hipSuccess;
-    if (a.S > 0 && a.tiles > 0) e = bf16 ? launch_rows<true>(a, false, stream) : launch_rows<false>(a, false, stream);
-    if (e != hipSuccess) return e;
-    if (a.S > 0) {
-        hipLaunchKernelGGL(moedisp_balance_seq, dim3(a.S), dim3(1024), 0, stream, a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.S > 0 && a.tiles > 0) {
+        const hipError_t e = launch_type(a, bf16, false, stream);
+        if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(moedisp_balance_loss, dim3(1), dim3(256), 0, stream, a);
+    const long long blocks = a.S > 0 ? (long long)a.S * ((a.E + kSeqCols - 1) / kSeqCols) : 1;
+    if (!grid_fits(blocks, kSeqThreads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(moedisp_balance_seq, dim3((unsigned)blocks), dim3(kSeqThreads), 0, stream, a);
     return hipGetLastError();
 }
 
 hipError_t launch_balance_backward(const BalanceArgs& a, bool bf16, hipStream_t stream) {
     if (a.S == 0 || a.tiles == 0) return hipSuccess;
-    return bf16 ? launch_rows<true>(a, true, stream) : launch_rows<false>(a, true, stream);
+    return launch_type(a, bf16, true, stream);
 }
 
 }  // namespace moedisp

@@ -95,18 +95,17 @@ size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 struct BalancePlan {
     int tile_tokens, tiles;
-    size_t psum, count, tokens, seq_loss, total;
+    size_t psum, count, tokens, part, some, total;
 };
 
-// Tiles of a sequence: about 512 over all sequences (two workgroups per
-// compute unit), whole passes of the rows that a workgroup takes at once.
+constexpr int kBalanceTiles = 2048;
+// Tiles of a sequence: about 2048 over all sequences (8 workgroups per
+// compute unit: 27 us for 131072 rows of 256 bf16 logits, 30 with 1024), whole passes of the rows that a workgroup takes at once.
 BalancePlan plan_balance(const moedisp_balance& b) {
     BalancePlan p;
     const long long S = b.num_seqs, L = b.seq_len, E = b.num_experts;
-    int lanes = 2;
-    while (lanes < 64 && lanes * 4 < E) lanes *= 2;
-    const long long once = 256 / lanes;
-    long long want = S > 0 ? (512 + S - 1) / S : 1;
+    const long long once = 256 / balance_lanes(b.num_experts);
+    long long want = S > 0 ? (kBalanceTiles + S - 1) / S : 1;
     long long tile = (L + want - 1) / want;
     tile = (tile + once - 1) / once * once;
     if (tile < once) tile = once;
@@ -116,8 +115,9 @@ BalancePlan plan_balance(const moedisp_balance& b) {
     p.psum = sizeof(WsHeader);
     p.count = round256(p.psum + all * E * 4);
     p.tokens = round256(p.count + all * E * 4);
-    p.seq_loss = round256(p.tokens + all * 4);
-    p.total = round256(p.seq_loss + (size_t)S * 4);
+    p.part = round256(p.tokens + all * 4);
+    p.some = round256(p.part + (size_t)S * ((E + 63) / 64) * 8);
+    p.total = round256(p.some + (size_t)S * 4);
     return p;
 }
 
@@ -262,7 +262,8 @@ int ep_balance_loss(const moedisp_balance* b, const void* logits, const int32_t*
     a.psum = (float*)((char*)ws + p.psum);
     a.count = (int32_t*)((char*)ws + p.count);
     a.tokens = (int32_t*)((char*)ws + p.tokens);
-    a.seq_loss = (float*)((char*)ws + p.seq_loss);
+    a.part = (double*)((char*)ws + p.part);
+    a.some = (int32_t*)((char*)ws + p.some);
     a.hdr = (WsHeader*)ws;
     return status_of(launch_balance(a, b->logits_dtype == MOEDISP_BF16, (hipStream_t)stream));
 }

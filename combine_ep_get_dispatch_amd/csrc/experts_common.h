@@ -193,11 +193,19 @@ struct BalanceArgs {
     float* psum;       // [S * tiles][E]
     int32_t* count;    // [S * tiles][E]
     int32_t* tokens;   // [S * tiles]
-    float* seq_loss;   // [S]
+    double* part;      // [S][ceil(E / 64)]: parts of the loss
+    int32_t* some;     // [S]: whether the sequence has tokens
     const float* d_loss;
     void* d_logits;
     WsHeader* hdr;
 };
+
+// Lanes that share a row of E logits, 8 experts each (more beyond 512).
+inline int balance_lanes(int E) {
+    int lanes = 1;
+    while (lanes < 64 && lanes * 8 < E) lanes *= 2;
+    return lanes;
+}
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, int scale_fmt, bool f32_out, bool accumulate,
                                hipStream_t stream);

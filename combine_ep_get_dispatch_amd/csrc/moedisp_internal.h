@@ -45,7 +45,7 @@ constexpr int kMaxBlockSlots = 512;        // >= kMaxBlockTokens * kMaxTopk
 // First 256 bytes of the workspace.
 struct WsHeader {
     uint32_t status;           // MOEDISP_DEV_* bits, or-ed by kernels
-    uint32_t reserved0;        // unused (kept zero)
+    uint32_t reserved0;        // workgroups done (balance loss); zero between calls
     uint32_t reserved[62];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
