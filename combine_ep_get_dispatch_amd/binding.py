@@ -286,29 +286,41 @@ class _Args:
             self.fail(f"{name} has dtype {str(t.dtype).replace('torch.', '')}, expected one of: {want}")
         if not t.is_contiguous():
             self.fail(f"{name} must be contiguous")
-        have = t.numel() * t.element_size()
+        have = t.nbytes
         if have < nbytes:
             self.fail(f"{name} holds {have} bytes, the shape needs {nbytes}")
-        self.tensors.append((name, t))
+        self.tensors.append((name, t, have))
 
     def done(self):
-        for name, t in self.tensors:
+        for name, t, _ in self.tensors:
             if t.device.type != "cuda":
                 self.fail(f"{name} is on {t.device}, expected a GPU tensor")
 
-    def on_device(self, stream):
+    def on_device(self, stream, *written):
         """As done(); every tensor must lie on one GPU, the stream's if one is
-        given.  Returns the device and its stream (the device's current one
-        unless one is given), so that the call does not depend on which
-        device is current."""
-        self.done()
-        dev = self.tensors[0][1].device
-        for name, t in self.tensors:
-            if t.device != dev:
-                self.fail(f"{name} is on {t.device}, {self.tensors[0][0]} on {dev}")
-        if stream is not None and stream.device != dev:
-            self.fail(f"the stream is on {stream.device}, the tensors on {dev}")
-        return dev, _s(stream if stream is not None else torch.cuda.current_stream(dev))
+        given, and the tensors named in `written` must share no memory with
+        any other.  Returns the GPU's index and the stream's handle (its
+        current stream unless one is given), so that the call does not depend
+        on which device is current."""
+        dev = self.tensors[0][1].get_device()
+        spans, out = [], []
+        for name, t, n in self.tensors:
+            at = t.data_ptr()
+            (out if name in written else spans).append((at, at + n, name))
+            if dev < 0 or t.get_device() != dev:
+                dev = -1
+        for i, (at, end, name) in enumerate(out):
+            for oat, oend, other in spans + out[i + 1:]:
+                if at < oend and oat < end:
+                    self.fail(f"{name} overlaps {other}")
+        if dev < 0:
+            self.done()
+            self.fail("the tensors lie on different GPUs: " + ", ".join(f"{n} on {t.device}" for n, t, _ in self.tensors))
+        if stream is None:
+            return dev, torch.cuda.current_stream(dev).cuda_stream
+        if stream.device.index != dev:
+            self.fail(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+        return dev, stream.cuda_stream
 
 
 def _dims(shape: moedisp_shape):
@@ -672,19 +684,19 @@ def _need_scales(A, name, t, fmt, count, optional=False):
     A.need(name, t, _F32 if fmt == SCALE_FP32 else (torch.uint8,), (4 if fmt == SCALE_FP32 else 1) * count, optional)
 
 
-def _apart(A, name, *others):
-    """The written tensor `name` must not share memory with the others."""
-    by = dict(A.tensors)
-    if name not in by:
-        return
-    def span(t):
-        return t.data_ptr(), t.data_ptr() + _nb(t)
-    a0, a1 = span(by[name])
-    for o in others:
-        if o in by and by[o].device == by[name].device:
-            b0, b1 = span(by[o])
-            if a0 < b1 and b0 < a1:
-                A.fail(f"{name} overlaps {o}")
+def _on(dev: int, call: str, *args):
+    """The C call with `dev` as the current device."""
+    f = getattr(_lib or load(), call)
+    if torch.cuda.current_device() == dev:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args)
+    _check(call, rc)
+
+
+def _a(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def ep_expert_gemm(rows, n, k, scale_fmt, x, x_scales, w, w_scales, row_bounds, y, out_dtype, ws, stream=None):
@@ -698,12 +710,9 @@ def ep_expert_gemm(rows, n, k, scale_fmt, x, x_scales, w, w_scales, row_bounds, 
     _need_scales(A, "w_scales", w_scales, scale_fmt, E * nb * kb)
     A.need("y", y, _out_dtypes(out_dtype), R * max(n, 0) * (4 if out_dtype == FP32 else 2))
     _ws(A, ws)
-    _apart(A, "y", "x", "x_scales", "w", "w_scales", "row_bounds", "ws")
-    dev, st = A.on_device(stream)
-    with torch.cuda.device(dev):
-        _check(A.call, load().ep_expert_gemm(
-            C.byref(rows), n, k, scale_fmt, _p(x), _p(x_scales), _p(w), _p(w_scales), _p(row_bounds), _p(y),
-            out_dtype, _p(ws), _nb(ws), st))
+    dev, st = A.on_device(stream, "y")
+    _on(dev, A.call, C.byref(rows), n, k, scale_fmt, _a(x), _a(x_scales), _a(w), _a(w_scales), _a(row_bounds),
+        _a(y), out_dtype, _a(ws), _nb(ws), st)
 
 
 def ep_expert_wgrad(rows, n, k, scale_fmt, x, x_scales, dy, row_bounds, dw, out_dtype, accumulate, ws, stream=None):
@@ -715,12 +724,9 @@ def ep_expert_wgrad(rows, n, k, scale_fmt, x, x_scales, dy, row_bounds, dw, out_
     A.need("dy", dy, _ROWS_BF16, R * max(n, 0) * 2)
     A.need("dw", dw, _out_dtypes(out_dtype), E * max(n, 0) * max(k, 0) * (4 if out_dtype == FP32 else 2))
     _ws(A, ws)
-    _apart(A, "dw", "x", "x_scales", "dy", "row_bounds", "ws")
-    dev, st = A.on_device(stream)
-    with torch.cuda.device(dev):
-        _check(A.call, load().ep_expert_wgrad(
-            C.byref(rows), n, k, scale_fmt, _p(x), _p(x_scales), _p(dy), _p(row_bounds), _p(dw), out_dtype,
-            1 if accumulate else 0, _p(ws), _nb(ws), st))
+    dev, st = A.on_device(stream, "dw")
+    _on(dev, A.call, C.byref(rows), n, k, scale_fmt, _a(x), _a(x_scales), _a(dy), _a(row_bounds), _a(dw),
+        out_dtype, 1 if accumulate else 0, _a(ws), _nb(ws), st)
 
 
 def ep_swiglu_quant(rows, inner, scale_fmt, gu, row_bounds, h, h_scales, ws, stream=None):
@@ -731,12 +737,9 @@ def ep_swiglu_quant(rows, inner, scale_fmt, gu, row_bounds, h, h_scales, ws, str
     A.need("h", h, _E4M3, R * I)
     _need_scales(A, "h_scales", h_scales, scale_fmt, R * (I // 128))
     _ws(A, ws)
-    _apart(A, "h", "gu", "h_scales", "row_bounds", "ws")
-    _apart(A, "h_scales", "gu", "row_bounds", "ws")
-    dev, st = A.on_device(stream)
-    with torch.cuda.device(dev):
-        _check(A.call, load().ep_swiglu_quant(
-            C.byref(rows), inner, scale_fmt, _p(gu), _p(row_bounds), _p(h), _p(h_scales), _p(ws), _nb(ws), st))
+    dev, st = A.on_device(stream, "h", "h_scales")
+    _on(dev, A.call, C.byref(rows), inner, scale_fmt, _a(gu), _a(row_bounds), _a(h), _a(h_scales), _a(ws),
+        _nb(ws), st)
 
 
 def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, dgu_scales, ws, stream=None):
@@ -749,14 +752,9 @@ def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, d
     A.need("dgu_q", dgu_q, _E4M3, R * I * 2, optional=True)
     _need_scales(A, "dgu_scales", dgu_scales, scale_fmt, R * (2 * I // 128), optional=True)
     _ws(A, ws)
-    _apart(A, "dgu", "gu", "dh", "dgu_q", "dgu_scales", "row_bounds", "ws")
-    _apart(A, "dgu_q", "gu", "dh", "dgu_scales", "row_bounds", "ws")
-    _apart(A, "dgu_scales", "gu", "dh", "row_bounds", "ws")
-    dev, st = A.on_device(stream)
-    with torch.cuda.device(dev):
-        _check(A.call, load().ep_swiglu_backward(
-            C.byref(rows), inner, scale_fmt, _p(gu), _p(dh), _p(row_bounds), _p(dgu), _p(dgu_q), _p(dgu_scales),
-            _p(ws), _nb(ws), st))
+    dev, st = A.on_device(stream, "dgu", "dgu_q", "dgu_scales")
+    _on(dev, A.call, C.byref(rows), inner, scale_fmt, _a(gu), _a(dh), _a(row_bounds), _a(dgu), _a(dgu_q),
+        _a(dgu_scales), _a(ws), _nb(ws), st)
 
 
 def ep_balance_workspace_bytes(balance) -> int:
@@ -779,13 +777,9 @@ def ep_balance_loss(balance, logits, topk_idx, loss, tokens_per_expert, tokens_p
     _need_balance(A, balance, logits, topk_idx, tokens_per_expert, tokens_per_seq)
     A.need("loss", loss, _F32, 4)
     _ws(A, ws)
-    for o in ("loss", "tokens_per_expert", "tokens_per_seq", "ws"):
-        _apart(A, o, "logits", "topk_idx", *(q for q in ("loss", "tokens_per_expert", "tokens_per_seq", "ws") if q != o))
-    dev, st = A.on_device(stream)
-    with torch.cuda.device(dev):
-        _check(A.call, load().ep_balance_loss(
-            C.byref(balance), _p(logits), _p(topk_idx), _p(loss), _p(tokens_per_expert), _p(tokens_per_seq), _p(ws),
-            _nb(ws), st))
+    dev, st = A.on_device(stream, "loss", "tokens_per_expert", "tokens_per_seq", "ws")
+    _on(dev, A.call, C.byref(balance), _a(logits), _a(topk_idx), _a(loss), _a(tokens_per_expert),
+        _a(tokens_per_seq), _a(ws), _nb(ws), st)
 
 
 def ep_balance_loss_backward(balance, logits, topk_idx, tokens_per_expert, tokens_per_seq, d_loss, d_logits,
@@ -794,12 +788,9 @@ def ep_balance_loss_backward(balance, logits, topk_idx, tokens_per_expert, token
     dt, nbytes = _need_balance(A, balance, logits, topk_idx, tokens_per_expert, tokens_per_seq)
     A.need("d_loss", d_loss, _F32, 4)
     A.need("d_logits", d_logits, dt, nbytes)
-    _apart(A, "d_logits", "logits", "topk_idx", "tokens_per_expert", "tokens_per_seq", "d_loss")
-    dev, st = A.on_device(stream)
-    with torch.cuda.device(dev):
-        _check(A.call, load().ep_balance_loss_backward(
-            C.byref(balance), _p(logits), _p(topk_idx), _p(tokens_per_expert), _p(tokens_per_seq), _p(d_loss),
-            _p(d_logits), st))
+    dev, st = A.on_device(stream, "d_logits")
+    _on(dev, A.call, C.byref(balance), _a(logits), _a(topk_idx), _a(tokens_per_expert), _a(tokens_per_seq),
+        _a(d_loss), _a(d_logits), st)
 
 
 def ep_check_status(ws, stream=None) -> int:
