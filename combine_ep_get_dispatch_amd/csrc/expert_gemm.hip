@@ -41,7 +41,7 @@ __device__ inline float scale_value(int bits) {
 __device__ inline int swizzle_w(int row) { return ((row >> 1) & 1) | (((row >> 3) & 3) << 1); }
 __device__ inline int swizzle_x(int row) { return (row >> 1) & 7; }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
+template <int BM, int BN, int WM, int WN, int WS, int XS, int FMT, bool F32>
 struct Tile {
     static constexpr int kWaves = WM * WN;
     static constexpr int kThreads = 64 * kWaves;
@@ -51,22 +51,29 @@ struct Tile {
     static constexpr int kNT = kN / 16;
     static constexpr int kWLoads = BN / 8 / kWaves;  // 1 KiB loads of a wave and stage
     static constexpr int kXLoads = (BM / 8 + kWaves - 1) / kWaves;
-    static constexpr int kLoads = kWLoads + kXLoads + 1;             // with one load of scales
+    // Loads of a wave and block, in this order: the rows of block kb + XS, one
+    // load of scales, the weights of block kb + WS.  Before block kb + 1 its
+    // rows have to be there, and all that is older; what is younger may be
+    // under way.
+    static constexpr int kLoads = kWLoads + kXLoads + 1;
+    static constexpr int kYounger = (WS > XS ? 1 + kWLoads : 0) + (XS - 2) * kLoads;
     static constexpr int kXBytes = kXLoads * kWaves * 1024;
-    static constexpr int kStage = BN * kBlk + kXBytes;
+    static constexpr int kWStage = BN * kBlk;
+    static constexpr int kStages = WS * kWStage + XS * kXBytes;
     // scales of the rows: chunks of kChunk blocks, two in LDS, [row][block]
     static constexpr int kSGroups = BM / 8;                             // loads of 8 rows by kChunk blocks
     static constexpr int kSTurns = (kSGroups + kWaves - 1) / kWaves;    // blocks in which a chunk is loaded
     static constexpr int kSBytes = 2 * BM * kChunk * 4 + kWaves * 256;  // and what the other blocks load
-    static_assert(kSTurns + STAGES <= kChunk, "a chunk is there before it is read");
+    static_assert(kSTurns + XS <= kChunk, "a chunk is there before it is read");
+    static_assert(WS >= XS && XS >= 2, "stages");
     static constexpr int kSwBlocks = BN >= kBlk ? BN / kBlk : 1;
-    static_assert(kNT % 2 == 0 && kM <= 64 && kM % 16 == 0 && kN % 32 == 0 && kN <= kBlk && BN % (8 * kWaves) == 0, "tile shape");
-    static constexpr size_t lds(int kb) { return (size_t)STAGES * kStage + kSBytes + (size_t)kSwBlocks * kb * 4; }
+    static_assert(kNT % 2 == 0 && kM % 16 == 0 && kN % 32 == 0 && kN <= kBlk && BN % (8 * kWaves) == 0, "tile shape");
+    static constexpr size_t lds(int kb) { return (size_t)kStages + kSBytes + (size_t)kSwBlocks * kb * 4; }
 };
 
-template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
+template <int BM, int BN, int WM, int WN, int WS, int XS, int FMT, bool F32>
 __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmArgs a) {
-    using T = Tile<BM, BN, WM, WN, STAGES, FMT, F32>;
+    using T = Tile<BM, BN, WM, WN, WS, XS, FMT, F32>;
     constexpr int SB = FMT == MOEDISP_SCALE_FP32 ? 4 : 1;
     extern __shared__ char lds[];
     const int tid = threadIdx.x;
@@ -117,7 +124,8 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         xoff[i] = min(row, rows - 1) * a.k + (((lane & 7) ^ swizzle_x(row)) << 4);
     }
     const int wm = wave % WM, wn = wave / WM;
-    char* const sx_lds = lds + STAGES * T::kStage;
+    char* const x_lds = lds + WS * T::kWStage;
+    char* const sx_lds = lds + T::kStages;
     // Scales of 8 rows (group g of the tile) and the 8 blocks of chunk ch: 32
     // bytes of each row at a time, as one scale of 64 rows costs a request
     // per lane.
@@ -126,17 +134,17 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         load_to_lds<SB>(srs, to, at * SB, 0);
     };
 
-    auto issue = [&](int kb, int buf) {
-        char* st = lds + buf * T::kStage;
+    auto issue_w = [&](int kb, int buf) {
 #pragma unroll
         for (int i = 0; i < T::kWLoads; ++i)
-            load_to_lds<16>(wrs, st + (wave * T::kWLoads + i) * 1024, woff[i], kb * kBlk);
+            load_to_lds<16>(wrs, lds + buf * T::kWStage + (wave * T::kWLoads + i) * 1024, woff[i], min(kb, a.kb - 1) * kBlk);
+    };
+    auto issue_x = [&](int kb, int buf) {
 #pragma unroll
         for (int i = 0; i < T::kXLoads; ++i)
-            load_to_lds<16>(xrs, st + BN * kBlk + (wave * T::kXLoads + i) * 1024, xoff[i], kb * kBlk);
+            load_to_lds<16>(xrs, x_lds + buf * T::kXBytes + (wave * T::kXLoads + i) * 1024, xoff[i],
+                            min(kb, a.kb - 1) * kBlk);
     };
-
-    wait_loads_and_sync<0>();  // the last tile's loads into LDS and reads of it are done
     char* const unused = sx_lds + 2 * BM * kChunk * 4 + wave * 256;
 
     // the weights' scales of the tile, all of k
@@ -160,9 +168,13 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         if (t * T::kWaves + wave < T::kSGroups)
             issue_scales(t * T::kWaves + wave, 0, sx_lds + (t * T::kWaves + wave) * 256);
 #pragma unroll
-    for (int p = 0; p < STAGES; ++p) {
-        issue(min(p, a.kb - 1), p);
-        issue_scales(0, 0, unused);  // as many loads as a later block has
+    for (int p = 0; p < WS; ++p) {
+        if (p >= WS - XS) {
+            issue_x(p - (WS - XS), p - (WS - XS));
+            issue_scales(0, 0, unused);  // as many loads as a later block has
+        }
+        issue_w(p, p);
+        __builtin_amdgcn_sched_barrier(0);
     }
 
     const int q = lane >> 4, c = lane & 15;
@@ -180,24 +192,26 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
     auto x_at = [&](const char* st, int kb, int j) {
         sxv[j] = reinterpret_cast<const int*>(
             sx_lds)[(((kb / kChunk) & 1) * BM + wm * T::kM + j * 16 + c) * kChunk + kb % kChunk];
-        return read_frag(st + BN * kBlk + (xrow + j * 16) * kBlk, xsw, q);
+        return read_frag(st + (xrow + j * 16) * kBlk, xsw, q);
     };
-    wait_loads_and_sync<(STAGES - 1) * T::kLoads>();
+    wait_loads_and_sync<T::kYounger + T::kLoads>();
     wf[0] = w_at(lds, 0);
 #pragma unroll
-    for (int j = 0; j < T::kMT; ++j) b[j] = x_at(lds, 0, j);
+    for (int j = 0; j < T::kMT; ++j) b[j] = x_at(x_lds, 0, j);
     // Block kb: its rows' operands and the first of the weights' are in
     // registers.  Product u = (i, j) is followed by the scaled add of the
     // product LAG before it, so that the matrix unit need not finish one
     // first; sched_barrier keeps this order.  Before the last i the block's
     // LDS has been read: the waves meet, its place is filled with the block
-    // STAGES later, and the next block's operands are read behind the last
+    // stages later, and the next block's operands are read behind the last
     // products.
-    int buf = 0;
+    int wbuf = 0, xbuf = 0;
     for (int kb = 0; kb < a.kb; ++kb) {
-        const char* st = lds + buf * T::kStage;
-        const int nbuf = buf + 1 == STAGES ? 0 : buf + 1;
-        const char* nst = lds + nbuf * T::kStage;
+        const char* st = lds + wbuf * T::kWStage;
+        const int nwbuf = wbuf + 1 == WS ? 0 : wbuf + 1;
+        const int nxbuf = xbuf + 1 == XS ? 0 : xbuf + 1;
+        const char* nst = lds + nwbuf * T::kWStage;
+        const char* nxt = x_lds + nxbuf * T::kXBytes;
         const int swv = swp[kb];
         float f[T::kMT];
         if (PROMOTE) {
@@ -213,14 +227,15 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
             if (u < U) {
                 if (j == 0 && i + 1 < T::kNT) wf[(i + 1) & 1] = w_at(st, i + 1);
                 if (u == U - T::kMT) {
-                    wait_loads_and_sync<(STAGES - 2) * T::kLoads>();
-                    issue(min(kb + STAGES, a.kb - 1), buf);
+                    wait_loads_and_sync<T::kYounger>();
+                    issue_x(kb + XS, xbuf);
                     // the next chunk of the rows' scales, in the first blocks
                     // of this one; later blocks load to a place of no use, so
                     // that every block has as many loads to wait for
                     const int g = kb % kChunk * T::kWaves + wave;
                     issue_scales(min(g, T::kSGroups - 1), kb / kChunk + 1,
                                  g < T::kSGroups ? sx_lds + (kb / kChunk + 1) % 2 * BM * kChunk * 4 + g * 256 : unused);
+                    issue_w(kb + WS, wbuf);
                     __builtin_amdgcn_sched_barrier(0);
                     wf[0] = w_at(nst, 0);
                 }
@@ -237,7 +252,7 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
                     p[u % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                         wf[i & 1], b[j], v4f{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
                 }
-                if (u >= U - T::kMT) b[j] = x_at(nst, kb + 1, j);
+                if (u >= U - T::kMT) b[j] = x_at(nxt, kb + 1, j);
             }
             if (PROMOTE && u >= LAG) {
                 const int io = (u - LAG) / T::kMT, jo = (u - LAG) % T::kMT;
@@ -247,7 +262,8 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        buf = nbuf;
+        wbuf = nwbuf;
+        xbuf = nxbuf;
     }
 
 #pragma unroll
@@ -275,9 +291,9 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
     wait_loads_and_sync<0>();  // no load may reach LDS after the workgroup's end
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int FMT, bool F32>
+template <int BM, int BN, int WM, int WN, int WS, int XS, int FMT, bool F32>
 hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
-    using T = Tile<BM, BN, WM, WN, STAGES, FMT, F32>;
+    using T = Tile<BM, BN, WM, WN, WS, XS, FMT, F32>;
     a.nt = (a.n + BN - 1) / BN;
     const long long tiles = (long long)a.r.max_rows / BM + a.r.E;  // at least the tiles of any bounds
     if (tiles * a.nt > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
@@ -286,24 +302,40 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
     long long blocks = (tiles * a.nt + kXcds - 1) / kXcds * kXcds;
     const long long resident = 256 * (kLdsBytes / (long long)lds);
     if (blocks > resident) blocks = resident;
-    hipLaunchKernelGGL((moedisp_expert_gemm<BM, BN, WM, WN, STAGES, FMT, F32>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((moedisp_expert_gemm<BM, BN, WM, WN, WS, XS, FMT, F32>), dim3((unsigned)blocks),
                        dim3(T::kThreads), lds, stream, a);
     return hipGetLastError();
 }
 
-// Tile by the rows an expert usually has.  Few rows: every weight is read
-// once per row tile whatever its height, so the tile is as flat as the rows
-// allow and several workgroups share a compute unit; many rows: the tile
-// whose loads per product are fewest.
+// Tile by the rows an expert usually has.  Every weight is read once per row
+// tile, so the tile holds the rows of a usual expert with some to spare, and
+// is no higher: the rows' loads take LDS from the weights' that come from HBM
+// (three blocks of weights and two of rows lie there).  Many rows: the tile
+// whose loads per product are fewest.  64 experts, K = N = 4096, us (fp32
+// scales, uniform routing):
+//     rows     32x128  64x256  96x256  128x256  160x256  256x256
+//       8       178      178     184     195      226      278
+//      24       199      185     187     196      226      275
+//      48       252      218     192     198      225      277
+//      96       362      249     255     217      239      285
+//     128        -       304     331     282      247      291
+//     192        -       393     377     371      464      299
+// Where the whole product is few tiles, the smallest spread it over the
+// device (24 experts of 125 rows, K = 640, N = 1000, fp32 results: 14.5 us
+// against 18.8 with 128 x 256).
 template <int FMT, bool F32>
 hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
-    if (mean_rows <= 8) return launch_tile<16, 128, 1, 4, 4, FMT, F32>(a, stream);
-    if (mean_rows <= 24) return launch_tile<32, 128, 1, 4, 3, FMT, F32>(a, stream);
-    if (mean_rows <= 48) return launch_tile<64, 256, 1, 4, 3, FMT, F32>(a, stream);
-    // (fp32 results keep widened operands in registers: the largest tile would spill)
-    if (mean_rows <= 192 || F32) return launch_tile<128, 256, 2, 4, 3, FMT, F32>(a, stream);
-    if constexpr (!F32) return launch_tile<256, 256, 4, 2, 2, FMT, F32>(a, stream);
-    return hipErrorInvalidConfiguration;  // not reached
+    const long long small = (long long)a.r.E * ((mean_rows + 31) / 32) * ((a.n + 127) / 128);
+    if (mean_rows <= 16 || small <= 1024) return launch_tile<32, 128, 1, 4, 3, 3, FMT, F32>(a, stream);
+    if (mean_rows <= 32) return launch_tile<64, 256, 2, 4, 3, 3, FMT, F32>(a, stream);
+    if (mean_rows <= 72) return launch_tile<96, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+    if constexpr (F32) {  // larger tiles' widened operands leave the registers
+        return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+    } else {
+        if (mean_rows <= 112) return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+        if (mean_rows <= 144) return launch_tile<160, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+        return launch_tile<256, 256, 4, 2, 2, 2, FMT, F32>(a, stream);
+    }
 }
 
 }  // namespace

@@ -77,6 +77,45 @@ def test_product_any_hint(fmt, expected):
         check_gemm(Problem([300, 0, 5, 64, 1], 392, 512, fmt, seed=3, expected=expected), out, f"hint {expected}")
 
 
+# experts from none to several tiles of any height, enough of them (and of
+# columns) that the tile goes by expected_rows
+WIDE = [(7 * e) % 5 for e in range(119)] + [33, 64, 65, 0, 97, 129, 160, 161, 257, 300, 0, 520]
+
+
+@pytest.mark.parametrize("K", [128, 640, 1152, 2176])
+@pytest.mark.parametrize("expected", [8, 24, 60, 100, 130, 300])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_product_every_tile(fmt, expected, K):
+    """Each tile shape, with one scale block, fewer than its stages, and past
+    one and two chunks of 8 blocks."""
+    p = Problem(WIDE, 1160, K, fmt, seed=K + expected, expected=expected)
+    for out in OUTS:
+        check_gemm(p, out, f"expected {expected} K {K} out {out}")
+
+
+def test_product_every_tile_padded():
+    for expected in (8, 24, 60, 100, 130, 300):
+        p = Problem(WIDE, 1160, 256, M.SCALE_FP32, seed=expected, padded=(310, 300, 7), expected=expected)
+        for out in OUTS:
+            check_gemm(p, out, f"expected {expected} out {out}")
+
+
+@pytest.mark.parametrize("out", OUTS)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_wgrad_large_tile(fmt, out):
+    """Enough tiles of 256 x 256 that they are taken, cut in both directions;
+    rows from none to several times round the stages."""
+    check_wgrad(Problem(WIDE, 264, 384, fmt, seed=9), out)
+
+
+def test_wgrad_large_tile_accumulates():
+    p = Problem(WIDE, 264, 384, M.SCALE_UE8M0, seed=10)
+    before = torch.randn(p.E, 264, 384, device="cuda")
+    dw = p.wgrad(M.FP32, True, before.clone())
+    want, s = p.wgrad64()
+    within(dw, want + before.double(), 530 * U * (s + before.abs().double()))
+
+
 @pytest.mark.parametrize("out", OUTS)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("padded", [(16, 16, 0), (24, 16, 8), (40, 33, 3), (8, 0, 0)])
@@ -582,9 +621,10 @@ def quantised_weights(g, E, N, K):
     return (b / sc[:, :, None, :, None]).view(E, N, K).to(E4M3), sc
 
 
-@pytest.mark.parametrize("layout", ["contiguous", "padded"])
-@pytest.mark.parametrize("fmt", FMTS)
-def test_experts_between_dispatch_and_combine(fmt, layout):
+# the padded dispatch moves binary32 scales
+@pytest.mark.parametrize("layout,fmt", [("contiguous", M.SCALE_FP32), ("contiguous", M.SCALE_UE8M0),
+                                        ("padded", M.SCALE_FP32)])
+def test_experts_between_dispatch_and_combine(layout, fmt):
     """Layout, quantising dispatch, both products with the activation between
     them, combine: the whole path as a serving program runs it, against 64
     bits on the same received codes."""
@@ -607,8 +647,6 @@ def test_experts_between_dispatch_and_combine(fmt, layout):
         rows, bounds = M.moedisp_rows.contiguous(E, T * k), bufs.expert_offsets
         xq, xsc, ws = bufs.recv_q, bufs.recv_qscales, bufs.ws
     else:
-        if fmt == M.SCALE_UE8M0:
-            pytest.skip("the padded dispatch moves binary32 scales")
         b = x.float().view(T, 2, 128)
         sc = b.abs().amax(-1) / 448
         codes = (b / sc[..., None]).view(T, H).to(E4M3)
