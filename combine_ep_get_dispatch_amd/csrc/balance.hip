@@ -121,32 +121,45 @@ __device__ inline float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 0x1.
 // is p[v] * the result.  For the sigmoid also the slopes 1 - s(z) if wanted.
 template <int LPR, int N, bool SLOPE>
 __device__ inline float row_scores(bool sigmoid, const float z[N], float p[N], float slope[N]) {
-    float sum = 0.0f, m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < N; ++v) m = fmaxf(m, z[v]);
-    m = lanes_max<LPR>(m);
+    float sum = 0.0f;
     if (sigmoid) {
 #pragma unroll
         for (int v = 0; v < N; ++v) {
             const float x = exp_of(-z[v]);
             p[v] = __builtin_amdgcn_rcpf(1.0f + x);
             if (SLOPE) slope[v] = z[v] >= 0.0f ? x * p[v] : 1.0f - p[v];
+            sum += p[v];
         }
-        // Where every logit is far below zero s(z) is exp(z) (1 - s(z)): the
-        // factor exp(-m) keeps the scores from vanishing together.
-        if (__any(m < -8.0f)) {
+        sum = lanes_sum<LPR>(sum);
+        // Where every logit is so far below zero that the scores vanish
+        // together, s(z) is exp(z): the factor exp(-m) keeps their ratios.
+        if (__any(sum < 0x1p-100f)) {
+            float m = -INFINITY, low = 0.0f;
 #pragma unroll
-            for (int v = 0; v < N; ++v)
-                if (m < -8.0f) p[v] = z[v] == -INFINITY ? 0.0f : exp_of(z[v] - m) * (1.0f - p[v]);
+            for (int v = 0; v < N; ++v) m = fmaxf(m, z[v]);
+            m = lanes_max<LPR>(m);
+#pragma unroll
+            for (int v = 0; v < N; ++v) {
+                const float x = z[v] == -INFINITY ? 0.0f : exp_of(z[v] - m);
+                if (sum < 0x1p-100f) p[v] = x;
+                low += x;
+            }
+            low = lanes_sum<LPR>(low);
+            if (sum < 0x1p-100f) sum = low;
         }
     } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < N; ++v) m = fmaxf(m, z[v]);
+        m = lanes_max<LPR>(m);
         m = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int v = 0; v < N; ++v) p[v] = exp_of(z[v] - m);
+        for (int v = 0; v < N; ++v) {
+            p[v] = exp_of(z[v] - m);
+            sum += p[v];
+        }
+        sum = lanes_sum<LPR>(sum);
     }
-#pragma unroll
-    for (int v = 0; v < N; ++v) sum += p[v];
-    sum = lanes_sum<LPR>(sum);
     return sum == 0.0f ? 0.0f : 1.0f / sum;  // no score at all: 0
 }
 
