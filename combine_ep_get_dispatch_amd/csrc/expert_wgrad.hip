@@ -1,5 +1,21 @@
 // Weight gradient of the experts' product:
 //     dw[e][n][k] (+)= sum over e's rows r of dy[r][n] * sx[r][k/128] * x[r][k]
+//
+// Precision.  The scales belong to rows, over which is summed, so they cannot
+// wait until after a matrix instruction: x becomes bf16, scale times code
+// rounded once (2^-8; exact for powers of two), and the products are those of
+// the bf16 instruction, added in binary32.
+//
+// What bounds it.  Many rows (32768 over 8 experts, 4096 x 4096): 1.07 ms, 1.0
+// PFLOP/s; products alone 0.78 ms, loads and LDS alone 0.91 ms.  Few rows (8192
+// over 64 experts, 7168 x 2048, fp32): the 3.8 GB of results, 0.96 ms, 4.0 TB/s.
+//
+// How.  A workgroup computes one tile over all rows of its expert, 32 rows a
+// step, three steps of loads under way.  Both operands are contracted over
+// rows, which is across the way they lie: LDS holds them by rows and the
+// transposing reads of the matrix operands turn them (registers that gather 8
+// rows a lane before LDS took 1.59 ms).  x passes through registers to be
+// widened, once per tile, between the products.
 #include "experts_common.h"
 
 namespace moedisp {
@@ -26,7 +42,7 @@ __device__ inline v4s read_transposed(const char* p) {
 
 // load_to_lds (experts_common.h) by an instruction that the compiler does not
 // see into: with the builtin it waits for every load into LDS before a
-// transposing read, and nothing could be loaded ahead (1372 us against 1115
+// transposing read, and nothing could be loaded ahead (1372 us against 1182
 // for 4096 x 4096 weights and 32768 rows).  There is no result register; the
 // waits are wait_loads_and_sync's and wait_own_loads'.  The leading s_nop
 // covers a descriptor that a vector instruction has just written.

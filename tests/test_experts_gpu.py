@@ -614,6 +614,79 @@ def test_replayed_graph_and_streams():
     assert p.status() == 0
 
 
+def test_calls_at_once():
+    """Calls of different workspaces on two streams at the same time, many
+    times over: each gives the bits that it gives alone."""
+    ps = [Problem([40, 0, 200, 3, 128], 520, 512, M.SCALE_FP32, seed=s, expected=100) for s in (61, 62)]
+    bal = [Balance(5, 300, 64, 4, M.SCORE_SOFTMAX) for _ in ps]
+    zs = [balance_inputs(5, 300, 64, 4, torch.float32, 63 + i) for i in range(2)]
+    alone = []
+    for p, b, (z, idx) in zip(ps, bal, zs):
+        b.forward(z, idx)
+        alone.append((p.gemm(M.BF16), p.wgrad(M.FP32), b.loss.clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    ys = [torch.full_like(a[0], 7.0) for a in alone]
+    dws = [torch.empty_like(a[1]) for a in alone]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, b, (z, idx), st, y, dw in zip(ps, bal, zs, streams, ys, dws):
+            M.ep_expert_gemm(p.rows, p.N, p.K, p.fmt, p.x, p.xs, p.w, p.ws_, p.bounds, y, M.BF16, p.ws, st)
+            M.ep_expert_wgrad(p.rows, p.N, p.K, p.fmt, p.x, p.xs, p.dy, p.bounds, dw, M.FP32, False, p.ws, st)
+            M.ep_balance_loss(b.b, z, idx, b.loss, b.counts, b.tokens, b.ws, st)
+    torch.cuda.synchronize()
+    for a, b, y, dw in zip(alone, bal, ys, dws):
+        assert torch.equal(a[0], y) and torch.equal(a[1], dw) and torch.equal(a[2], b.loss)
+
+
+def test_training_step_through_the_experts():
+    """Forward, then the gradients of rows, both weights and the gate inputs
+    as a training program makes them (quantised gradients feed the product of
+    the transposed weights), against 64-bit autograd of the same dequantised
+    values."""
+    counts, H, I = [33, 0, 70, 5], 256, 256
+    p = Problem(counts, 2 * I, H, M.SCALE_FP32, seed=71, spare=0)
+    q = Problem(counts, H, I, M.SCALE_FP32, seed=72, spare=0)
+    R, rows = p.R, p.rows
+    gu = p.gemm(M.BF16)
+    scale = 3.0 / gu.float().abs().max()        # gates of ordinary size: the scale goes into the weights
+    p.ws_.mul_(scale)
+    gu = p.gemm(M.BF16)
+    h, hs = torch.empty(R, I, dtype=torch.uint8, device="cuda").view(E4M3), torch.empty(R, I // 128, device="cuda")
+    M.ep_swiglu_quant(rows, I, p.fmt, gu, p.bounds, h, hs, p.ws)
+    dy = torch.randn(R, H, device="cuda").to(torch.bfloat16)
+    b = dy.float().view(R, H // 128, 128)
+    dys = b.abs().amax(-1) / 448
+    dyq = (b / dys[..., None]).view(R, H).to(E4M3)
+    w2t, w2ts = q.w.view(torch.uint8).transpose(1, 2).contiguous().view(E4M3), q.ws_.transpose(1, 2).contiguous()
+    dh = torch.empty(R, I, dtype=torch.bfloat16, device="cuda")
+    M.ep_expert_gemm(rows, I, H, p.fmt, dyq, dys, w2t, w2ts, p.bounds, dh, M.BF16, p.ws)
+    dw2 = torch.empty(4, H, I, device="cuda")
+    M.ep_expert_wgrad(rows, H, I, p.fmt, h, hs, dy, p.bounds, dw2, M.FP32, False, p.ws)
+    dgu = torch.empty(R, 2 * I, dtype=torch.bfloat16, device="cuda")
+    dq, dqs = torch.empty(R, 2 * I, dtype=torch.uint8, device="cuda").view(E4M3), torch.empty(R, 2 * I // 128, device="cuda")
+    M.ep_swiglu_backward(rows, I, p.fmt, gu, dh, p.bounds, dgu, dq, dqs, p.ws)
+    w1t, w1ts = p.w.view(torch.uint8).transpose(1, 2).contiguous().view(E4M3), p.ws_.transpose(1, 2).contiguous()
+    dx = torch.empty(R, H, dtype=torch.bfloat16, device="cuda")
+    M.ep_expert_gemm(rows, H, 2 * I, p.fmt, dq, dqs, w1t, w1ts, p.bounds, dx, M.BF16, p.ws)
+    dw1 = torch.empty(4, 2 * I, H, device="cuda")
+    M.ep_expert_wgrad(rows, 2 * I, H, p.fmt, p.x, p.xs, dgu, p.bounds, dw1, M.FP32, False, p.ws)
+    assert p.status() == 0
+    for e, (lo, c) in enumerate(p.spans):
+        x = rows64(p.x[lo:lo + c], p.xs[lo:lo + c]).requires_grad_()
+        w1 = weights64(p.w[e], p.ws_[e]).requires_grad_()
+        w2 = weights64(q.w[e], q.ws_[e]).requires_grad_()
+        (swiglu64(x @ w1.t()) @ w2.t()).backward(dy[lo:lo + c].double())
+        # every path passes at most two E4M3 roundings (2^-4 each at worst, about a third of that in the norm)
+        # and bf16 ones: as whole vectors the gradients agree to 2^-4
+        for name, got, want in (("dx", dx[lo:lo + c], x.grad), ("dw1", dw1[e], w1.grad), ("dw2", dw2[e], w2.grad)):
+            if c == 0:
+                assert got.numel() == 0 or (got == 0).all()
+            else:
+                off = float((got.double() - want).norm() / want.norm())
+                assert off < 2.0 ** -4, (e, name, off)
+
+
 def quantised_weights(g, E, N, K):
     w = torch.randn(E, N, K, generator=g).cuda() / K ** 0.5
     b = w.view(E, N // 128, 128, K // 128, 128)
