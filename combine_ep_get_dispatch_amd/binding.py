@@ -269,7 +269,7 @@ class _Args:
 
     def __init__(self, call: str):
         self.call = call
-        self.tensors = []
+        self.tensors, self.read, self.out = [], [], []
 
     def fail(self, msg: str):
         raise MoeDispError(self.call, ERR_INVALID_ARG, msg)
@@ -296,24 +296,39 @@ class _Args:
             if t.device.type != "cuda":
                 self.fail(f"{name} is on {t.device}, expected a GPU tensor")
 
-    def on_device(self, stream, *written):
-        """As done(); every tensor must lie on one GPU, the stream's if one is
-        given, and the tensors named in `written` must share no memory with
-        any other.  Returns the GPU's index and the stream's handle (its
-        current stream unless one is given), so that the call does not depend
-        on which device is current."""
+    def arg(self, name: str, t, dtypes, nbytes: int, optional: bool = False, written: bool = False):
+        """As need(); returns the tensor's address (None for none).  The call
+        writes to a tensor that is `written`."""
+        if type(t) is torch.Tensor and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
+            have = t.nbytes
+            if have < nbytes:
+                self.need(name, t, dtypes, nbytes, optional)  # says so
+            self.tensors.append((name, t, have))
+        else:
+            self.need(name, t, dtypes, nbytes, optional)  # takes a subclass or none, else says what is wrong
+            if t is None:
+                return None
+            have = t.nbytes
+        at = t.data_ptr()
+        (self.out if written else self.read).append((at, at + have, name))
+        return at
+
+    def on_device(self, stream):
+        """As done(), for arguments taken by arg(); every tensor must lie on
+        one GPU, the stream's if one is given, and those written must share no
+        memory with any other.  Returns the GPU's index and the stream's
+        handle (its current stream unless one is given), so that the call does
+        not depend on which device is current."""
         dev = self.tensors[0][1].get_device()
-        spans, out = [], []
-        for name, t, n in self.tensors:
-            at = t.data_ptr()
-            (out if name in written else spans).append((at, at + n, name))
-            if dev < 0 or t.get_device() != dev:
-                dev = -1
-        for i, (at, end, name) in enumerate(out):
-            for oat, oend, other in spans + out[i + 1:]:
+        same = dev >= 0
+        for _, t, _ in self.tensors:
+            if t.get_device() != dev:
+                same = False
+        for i, (at, end, name) in enumerate(self.out):
+            for oat, oend, other in self.read + self.out[i + 1:]:
                 if at < oend and oat < end:
                     self.fail(f"{name} overlaps {other}")
-        if dev < 0:
+        if not same:
             self.done()
             self.fail("the tensors lie on different GPUs: " + ", ".join(f"{n} on {t.device}" for n, t, _ in self.tensors))
         if stream is None:
@@ -670,18 +685,21 @@ def ep_combine_padded(shape, expert_stride, expert_out, recv_src_idx, recv_weigh
         _p(out), int(out_dtype), _p(ws), _nb(ws), _s(stream)))
 
 
-_E4M3 = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+_U8 = (torch.uint8,)
+_BF16 = (torch.bfloat16,)
 
 
-def _need_rows(A, rows, row_bounds):
-    """max_rows, after checking the bounds' size."""
+def _rows_of(A, rows, row_bounds):
+    """max_rows, the expert count and the bounds' address."""
     E = max(rows.num_experts, 0)
-    A.need("row_bounds", row_bounds, _INT32, 4 * (E + (0 if rows.expert_stride > 0 else 1)))
-    return max(rows.max_rows, 0)
+    return max(rows.max_rows, 0), E, A.arg("row_bounds", row_bounds, _INT32,
+                                           4 * (E + (0 if rows.expert_stride > 0 else 1)))
 
 
-def _need_scales(A, name, t, fmt, count, optional=False):
-    A.need(name, t, _F32 if fmt == SCALE_FP32 else (torch.uint8,), (4 if fmt == SCALE_FP32 else 1) * count, optional)
+def _scales(A, name, t, fmt, count, optional=False, written=False):
+    if fmt == SCALE_FP32:
+        return A.arg(name, t, _F32, 4 * count, optional, written)
+    return A.arg(name, t, _U8, count, optional, written)
 
 
 def _on(dev: int, call: str, *args):
@@ -692,105 +710,95 @@ def _on(dev: int, call: str, *args):
     else:
         with torch.cuda.device(dev):
             rc = f(*args)
-    _check(call, rc)
-
-
-def _a(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+    if rc != OK:
+        _check(call, rc)
 
 
 def ep_expert_gemm(rows, n, k, scale_fmt, x, x_scales, w, w_scales, row_bounds, y, out_dtype, ws, stream=None):
     A = _Args("ep_expert_gemm")
     n, k, scale_fmt, out_dtype = int(n), int(k), int(scale_fmt), int(out_dtype)
-    R, E = _need_rows(A, rows, row_bounds), max(rows.num_experts, 0)
-    kb, nb = max(k, 0) // 128, (max(n, 0) + 127) // 128
-    A.need("x", x, _E4M3, R * max(k, 0))
-    _need_scales(A, "x_scales", x_scales, scale_fmt, R * kb)
-    A.need("w", w, _E4M3, E * max(n, 0) * max(k, 0))
-    _need_scales(A, "w_scales", w_scales, scale_fmt, E * nb * kb)
-    A.need("y", y, _out_dtypes(out_dtype), R * max(n, 0) * (4 if out_dtype == FP32 else 2))
-    _ws(A, ws)
-    dev, st = A.on_device(stream, "y")
-    _on(dev, A.call, C.byref(rows), n, k, scale_fmt, _a(x), _a(x_scales), _a(w), _a(w_scales), _a(row_bounds),
-        _a(y), out_dtype, _a(ws), _nb(ws), st)
+    R, E, bounds = _rows_of(A, rows, row_bounds)
+    N, K = max(n, 0), max(k, 0)
+    kb = K // 128
+    args = (A.arg("x", x, _ROWS_FP8, R * K), _scales(A, "x_scales", x_scales, scale_fmt, R * kb),
+            A.arg("w", w, _ROWS_FP8, E * N * K),
+            _scales(A, "w_scales", w_scales, scale_fmt, E * ((N + 127) // 128) * kb), bounds,
+            A.arg("y", y, _out_dtypes(out_dtype), R * N * (4 if out_dtype == FP32 else 2), written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), n, k, scale_fmt, *args, out_dtype, at, ws.nbytes, st)
 
 
 def ep_expert_wgrad(rows, n, k, scale_fmt, x, x_scales, dy, row_bounds, dw, out_dtype, accumulate, ws, stream=None):
     A = _Args("ep_expert_wgrad")
     n, k, scale_fmt, out_dtype = int(n), int(k), int(scale_fmt), int(out_dtype)
-    R, E = _need_rows(A, rows, row_bounds), max(rows.num_experts, 0)
-    A.need("x", x, _E4M3, R * max(k, 0))
-    _need_scales(A, "x_scales", x_scales, scale_fmt, R * (max(k, 0) // 128))
-    A.need("dy", dy, _ROWS_BF16, R * max(n, 0) * 2)
-    A.need("dw", dw, _out_dtypes(out_dtype), E * max(n, 0) * max(k, 0) * (4 if out_dtype == FP32 else 2))
-    _ws(A, ws)
-    dev, st = A.on_device(stream, "dw")
-    _on(dev, A.call, C.byref(rows), n, k, scale_fmt, _a(x), _a(x_scales), _a(dy), _a(row_bounds), _a(dw),
-        out_dtype, 1 if accumulate else 0, _a(ws), _nb(ws), st)
+    R, E, bounds = _rows_of(A, rows, row_bounds)
+    N, K = max(n, 0), max(k, 0)
+    args = (A.arg("x", x, _ROWS_FP8, R * K), _scales(A, "x_scales", x_scales, scale_fmt, R * (K // 128)),
+            A.arg("dy", dy, _ROWS_BF16, R * N * 2), bounds,
+            A.arg("dw", dw, _out_dtypes(out_dtype), E * N * K * (4 if out_dtype == FP32 else 2), written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), n, k, scale_fmt, *args, out_dtype, 1 if accumulate else 0, at, ws.nbytes, st)
 
 
 def ep_swiglu_quant(rows, inner, scale_fmt, gu, row_bounds, h, h_scales, ws, stream=None):
     A = _Args("ep_swiglu_quant")
     inner, scale_fmt = int(inner), int(scale_fmt)
-    R, I = _need_rows(A, rows, row_bounds), max(inner, 0)
-    A.need("gu", gu, _ROWS_BF16, R * I * 4)
-    A.need("h", h, _E4M3, R * I)
-    _need_scales(A, "h_scales", h_scales, scale_fmt, R * (I // 128))
-    _ws(A, ws)
-    dev, st = A.on_device(stream, "h", "h_scales")
-    _on(dev, A.call, C.byref(rows), inner, scale_fmt, _a(gu), _a(row_bounds), _a(h), _a(h_scales), _a(ws),
-        _nb(ws), st)
+    R, _, bounds = _rows_of(A, rows, row_bounds)
+    I = max(inner, 0)
+    args = (A.arg("gu", gu, _ROWS_BF16, R * I * 4), bounds, A.arg("h", h, _ROWS_FP8, R * I, written=True),
+            _scales(A, "h_scales", h_scales, scale_fmt, R * (I // 128), written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), inner, scale_fmt, *args, at, ws.nbytes, st)
 
 
 def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, dgu_scales, ws, stream=None):
     A = _Args("ep_swiglu_backward")
     inner, scale_fmt = int(inner), int(scale_fmt)
-    R, I = _need_rows(A, rows, row_bounds), max(inner, 0)
-    A.need("gu", gu, _ROWS_BF16, R * I * 4)
-    A.need("dh", dh, _ROWS_BF16, R * I * 2)
-    A.need("dgu", dgu, _ROWS_BF16, R * I * 4, optional=True)
-    A.need("dgu_q", dgu_q, _E4M3, R * I * 2, optional=True)
-    _need_scales(A, "dgu_scales", dgu_scales, scale_fmt, R * (2 * I // 128), optional=True)
-    _ws(A, ws)
-    dev, st = A.on_device(stream, "dgu", "dgu_q", "dgu_scales")
-    _on(dev, A.call, C.byref(rows), inner, scale_fmt, _a(gu), _a(dh), _a(row_bounds), _a(dgu), _a(dgu_q),
-        _a(dgu_scales), _a(ws), _nb(ws), st)
+    R, _, bounds = _rows_of(A, rows, row_bounds)
+    I = max(inner, 0)
+    args = (A.arg("gu", gu, _ROWS_BF16, R * I * 4), A.arg("dh", dh, _ROWS_BF16, R * I * 2), bounds,
+            A.arg("dgu", dgu, _ROWS_BF16, R * I * 4, optional=True, written=True),
+            A.arg("dgu_q", dgu_q, _ROWS_FP8, R * I * 2, optional=True, written=True),
+            _scales(A, "dgu_scales", dgu_scales, scale_fmt, R * (2 * I // 128), optional=True, written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), inner, scale_fmt, *args, at, ws.nbytes, st)
 
 
 def ep_balance_workspace_bytes(balance) -> int:
     return int(load().ep_balance_workspace_bytes(C.byref(balance)))
 
 
-def _need_balance(A, b, logits, topk_idx, tokens_per_expert, tokens_per_seq):
+def _router(A, b, logits, topk_idx):
+    """S, E, the logits' types and bytes, and the two addresses."""
     S, L, E, k = max(b.num_seqs, 0), max(b.seq_len, 0), max(b.num_experts, 0), max(b.topk, 0)
-    dt = (torch.bfloat16,) if b.logits_dtype == BF16 else _F32
-    nbytes = S * L * E * (2 if b.logits_dtype == BF16 else 4)
-    A.need("logits", logits, dt, nbytes)
-    A.need("topk_idx", topk_idx, _INT32, 4 * S * L * k)
-    A.need("tokens_per_expert", tokens_per_expert, _INT32, 4 * S * E)
-    A.need("tokens_per_seq", tokens_per_seq, _INT32, 4 * S)
-    return dt, nbytes
+    dt, nbytes = (_BF16, S * L * E * 2) if b.logits_dtype == BF16 else (_F32, S * L * E * 4)
+    return S, E, dt, nbytes, A.arg("logits", logits, dt, nbytes), A.arg("topk_idx", topk_idx, _INT32, 4 * S * L * k)
 
 
 def ep_balance_loss(balance, logits, topk_idx, loss, tokens_per_expert, tokens_per_seq, ws, stream=None):
     A = _Args("ep_balance_loss")
-    _need_balance(A, balance, logits, topk_idx, tokens_per_expert, tokens_per_seq)
-    A.need("loss", loss, _F32, 4)
-    _ws(A, ws)
-    dev, st = A.on_device(stream, "loss", "tokens_per_expert", "tokens_per_seq", "ws")
-    _on(dev, A.call, C.byref(balance), _a(logits), _a(topk_idx), _a(loss), _a(tokens_per_expert),
-        _a(tokens_per_seq), _a(ws), _nb(ws), st)
+    S, E, _, _, z, idx = _router(A, balance, logits, topk_idx)
+    args = (z, idx, A.arg("loss", loss, _F32, 4, written=True),
+            A.arg("tokens_per_expert", tokens_per_expert, _INT32, 4 * S * E, written=True),
+            A.arg("tokens_per_seq", tokens_per_seq, _INT32, 4 * S, written=True),
+            A.arg("ws", ws, _BYTES, 1, written=True))
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(balance), *args, ws.nbytes, st)
 
 
 def ep_balance_loss_backward(balance, logits, topk_idx, tokens_per_expert, tokens_per_seq, d_loss, d_logits,
                              stream=None):
     A = _Args("ep_balance_loss_backward")
-    dt, nbytes = _need_balance(A, balance, logits, topk_idx, tokens_per_expert, tokens_per_seq)
-    A.need("d_loss", d_loss, _F32, 4)
-    A.need("d_logits", d_logits, dt, nbytes)
-    dev, st = A.on_device(stream, "d_logits")
-    _on(dev, A.call, C.byref(balance), _a(logits), _a(topk_idx), _a(tokens_per_expert), _a(tokens_per_seq),
-        _a(d_loss), _a(d_logits), st)
+    S, E, dt, nbytes, z, idx = _router(A, balance, logits, topk_idx)
+    args = (z, idx, A.arg("tokens_per_expert", tokens_per_expert, _INT32, 4 * S * E),
+            A.arg("tokens_per_seq", tokens_per_seq, _INT32, 4 * S), A.arg("d_loss", d_loss, _F32, 4),
+            A.arg("d_logits", d_logits, dt, nbytes, written=True))
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(balance), *args, st)
 
 
 def ep_check_status(ws, stream=None) -> int:
