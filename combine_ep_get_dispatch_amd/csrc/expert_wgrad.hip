@@ -88,7 +88,7 @@ struct WTile {
     static constexpr int kOps = kDyLoads + 2;                  // loads of a wave and step
     static constexpr int kXRaw = 1024 + 256;                   // a wave's codes and scales of a step
     static constexpr int kLds = kStages * (kDyStage + kWaves * kXRaw) + 2 * kXStage;
-    static_assert(kKT >= 4 && kXRows * kWaves == kStep && kDyRow >= 256 && kXRow >= 256, "tile shape");
+    static_assert(kKT >= 4 && kKT % 2 == 0 && kXRows * kWaves == kStep && kDyRow >= 256 && kXRow >= 256, "tile shape");
 };
 
 template <int TN, int TK, int WN, int WK, int FMT, bool F32, bool ADD>
@@ -158,9 +158,16 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
         load_to_lds_unseen<SB>((const char*)a.x_scales + ((size_t)first + r0) * a.kb * SB, raw + u * T::kXRaw + 1024,
                                (row * a.kb + x_ch / kScaleBlock) * SB);
     };
+    // bf16 results: unit 2p holds channels 0-3, 8-11, 16-19, 24-27 of 32 and
+    // unit 2p + 1 the others, so that two products give a lane 8 neighbours,
+    // 16 bytes to store (4 lanes 64 bytes; in order it would be 32)
+    constexpr bool kPairs = !F32;
     char* const x_lds = lds + kStages * T::kDyStage;
-    const int x_at = x_row * T::kXRow + ((lane % T::kXLanes) ^ unit_swizzle(x_row)) * 32;
-    const int x_half = (lane >> 3) & 1;  // of the 32 bytes, which 16 first: 8 neighbours fill different banks
+    const int x_unit = lane % T::kXLanes, x_sw = unit_swizzle(x_row);
+    const int x_at[2] = {
+        x_row * T::kXRow + (kPairs ? ((x_unit & ~1) ^ x_sw) * 32 + (x_unit & 1) * 16 : (x_unit ^ x_sw) * 32),
+        x_row * T::kXRow + (kPairs ? ((x_unit | 1) ^ x_sw) * 32 + (x_unit & 1) * 16 : (x_unit ^ x_sw) * 32 + 16)};
+    const bool x_half = lane & 8;  // which 16 bytes first: 16 neighbours fill different banks
     auto stage_x = [&](int step, int u) {
         const v4u xr = *reinterpret_cast<const v4u*>(raw + u * T::kXRaw + lane * 16);
         const int xs = *reinterpret_cast<const int*>(raw + u * T::kXRaw + 1024 + lane * 4);
@@ -174,9 +181,14 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
             o[i >> 1][2 * (i & 1)] = pack_bf16x2(lo.x * s, lo.y * s) & on;
             o[i >> 1][2 * (i & 1) + 1] = pack_bf16x2(hi.x * s, hi.y * s) & on;
         }
-        char* to = x_lds + (step & 1) * T::kXStage + x_at;
-        *reinterpret_cast<v4u*>(to + x_half * 16) = x_half ? o[1] : o[0];
-        *reinterpret_cast<v4u*>(to + (x_half ^ 1) * 16) = x_half ? o[0] : o[1];
+        if (kPairs) {
+            const v4u t = {o[0][0], o[0][1], o[1][0], o[1][1]};
+            o[1] = v4u{o[0][2], o[0][3], o[1][2], o[1][3]};
+            o[0] = t;
+        }
+        char* to = x_lds + (step & 1) * T::kXStage;
+        *reinterpret_cast<v4u*>(to + (x_half ? x_at[1] : x_at[0])) = x_half ? o[1] : o[0];
+        *reinterpret_cast<v4u*>(to + (x_half ? x_at[0] : x_at[1])) = x_half ? o[0] : o[1];
     };
 
     const int wk = wave % WK * (TK / WK), wn = wave / WK * (TN / WN);
@@ -244,19 +256,23 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
     for (int j = 0; j < T::kNT; ++j) {
         const int n = n0 + wn + j * 16 + c;
         if (n >= a.n) continue;
+        if (F32) {
 #pragma unroll
-        for (int i = 0; i < T::kKT; ++i) {
-            const int k = k0 + wk + i * 16 + q * 4;
-            if (k >= a.k) continue;
-            const size_t at = ((size_t)e * a.n + n) * a.k + k;
-            v4f v = acc[i][j];
-            if (F32) {
-                v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.dw) + at);
-                if (ADD) v += *o;
-                *o = v;
-            } else {
-                *reinterpret_cast<v2i*>(reinterpret_cast<uint16_t*>(a.dw) + at) =
-                    v2i{(int)pack_bf16x2(v[0], v[1]), (int)pack_bf16x2(v[2], v[3])};
+            for (int i = 0; i < T::kKT; ++i) {
+                const int k = k0 + wk + i * 16 + q * 4;
+                if (k >= a.k) continue;
+                v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.dw) + ((size_t)e * a.n + n) * a.k + k);
+                *o = ADD ? acc[i][j] + *o : acc[i][j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < T::kKT; i += 2) {
+                const int k = k0 + wk + i * 16 + q * 8;
+                if (k >= a.k) continue;
+                const v4f lo = acc[i][j], hi = acc[i + 1][j];
+                *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.dw) + ((size_t)e * a.n + n) * a.k + k) =
+                    v4u{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                        pack_bf16x2(hi[2], hi[3])};
             }
         }
     }
@@ -274,15 +290,20 @@ hipError_t launch_one(ExpertWgradArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Tiles of 256 x 256 move the fewest bytes per product; where they would not
-// give every compute unit one, tiles of 128 x 128 (two workgroups to a unit):
-// 8 experts of 512 x 512 and 1024 rows 24 us against 47, but 8 of 1024 x 2048
-// (256 large tiles) 49 us large against 64 small.
+// Tiles of 256 x 256 move the fewest bytes per product (8 experts of 4096 x
+// 4096 and 4096 rows each: 1069 us against 1459 with 128 x 128).  Tiles of 128 x
+// 128 (two workgroups to a unit) where large ones, in whole rounds of one for
+// each unit, cover a fifth more than small ones do: 8 experts of 512 x 512 and
+// 1024 rows each 24 us against 47, 52 of 2008 x 128 26 against 33, 13 of 1048
+// x 3328 42 against 51; not 35 of 3264 x 1536 (1.03 times as much), 164 against
+// 179.
 template <int FMT, bool F32, bool ADD>
 hipError_t launch_tiles(const ExpertWgradArgs& a, hipStream_t stream) {
     const long long large = (long long)a.r.E * ((a.n + 255) / 256) * ((a.k + 255) / 256);
-    return large >= 256 ? launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream)
-                        : launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
+    const long long small = (long long)a.r.E * ((a.n + 127) / 128) * ((a.k + 127) / 128);
+    const long long rounds = (large + kCus - 1) / kCus * kCus;
+    return rounds * 4 * 5 <= small * 6 ? launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream)
+                                       : launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
 }
 
 template <int FMT>

@@ -7,6 +7,7 @@
 
 namespace moedisp {
 
+constexpr int kCus = 256;          // compute units
 constexpr int kScaleBlock = 128;  // channels per scale
 
 // moedisp_rows for the device.
