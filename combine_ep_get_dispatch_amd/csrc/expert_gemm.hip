@@ -65,7 +65,7 @@ __device__ inline float scale_value(int bits) {
 
 // LDS reads of 16 bytes go in groups of 16 lanes ({0-3, 12-15, 20-27} and its
 // like) over 64 banks.  Rows of an operand read: 0-3, 8-11, 16-19, 24-27 for
-// the weights (see the columns' order), 0-15 for the tokens.
+// the weights of bf16 results (see the columns' order), else 0-15.
 __device__ inline int swizzle_w(int row) { return ((row >> 1) & 1) | (((row >> 3) & 3) << 1); }
 __device__ inline int swizzle_x(int row) { return (row >> 1) & 7; }
 
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
 #pragma unroll
         for (int i = 0; i < T::kWLoads; ++i) {
             const int row = (wave * T::kWLoads + i) * 8 + (lane >> 3);
-            woff[i] = min(row, cols - 1) * a.k + (((lane & 7) ^ swizzle_w(row)) << 4);
+            woff[i] = min(row, cols - 1) * a.k + (((lane & 7) ^ (F32 ? swizzle_x(row) : swizzle_w(row))) << 4);
         }
 #pragma unroll
         for (int i = 0; i < T::kXLoads; ++i) {
@@ -207,16 +207,18 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
         }
 
         const int q = lane >> 4, c = lane & 15;
-        const int wrow = wn * T::kN + (c >> 2) * 8 + (c & 3);
+        // columns of products 2t and 2t + 1 that a lane gets: bf16 results 8
+        // neighbours, fp32 results 4 of each, 16 bytes to store either way
+        const int wrow = wn * T::kN + (F32 ? c : (c >> 2) * 8 + (c & 3));
         const int xrow = wm * T::kM + c;
-        const int wsw = swizzle_w(wrow), xsw = swizzle_x(xrow);
+        const int wsw = F32 ? swizzle_x(wrow) : swizzle_w(wrow), xsw = swizzle_x(xrow);
         // scale of the block's partial sums; the power-of-two scales of bf16
         // results go into the matrix instruction
         constexpr bool PROMOTE = FMT == MOEDISP_SCALE_FP32 || F32;
         v8i b[T::kMT], wf[2];
         int sxv[T::kMT];
         auto w_at = [&](const char* st, int i) {
-            return read_frag(st + (wrow + (i >> 1) * 32 + (i & 1) * 4) * kBlk, wsw, q);
+            return read_frag(st + (wrow + (F32 ? i * 16 : (i >> 1) * 32 + (i & 1) * 4)) * kBlk, wsw, q);
         };
         auto x_at = [&](const char* st, int kb, int j) {
             sxv[j] = reinterpret_cast<const int*>(
@@ -305,16 +307,14 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm(ExpertGemmAr
             const int m = wm * T::kM + j * 16 + c;
             if (m >= rows) continue;
 #pragma unroll
-            for (int t = 0; t < T::kNT / 2; ++t) {
-                const int n = wn * T::kN + t * 32 + q * 8;
+            for (int t = 0; t < T::kNT; t += F32 ? 1 : 2) {
+                const int n = wn * T::kN + t * 16 + q * (F32 ? 4 : 8);
                 if (n >= cols) continue;
                 const size_t at = (row0 + m) * a.n + n0 + n;
-                const v4f lo = acc[2 * t][j], hi = acc[2 * t + 1][j];
                 if (F32) {
-                    v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at);
-                    o[0] = lo;
-                    o[1] = hi;
+                    *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at) = acc[t][j];
                 } else {
+                    const v4f lo = acc[t][j], hi = acc[t + 1][j];
                     const v4u v = {pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
                                    pack_bf16x2(hi[2], hi[3])};
                     *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.y) + at) = v;
@@ -333,7 +333,7 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
     static_assert(T::lds(512) <= kLdsBytes, "65536 channels");
     const size_t lds = T::lds(a.kb);
     long long blocks = (tiles * a.nt + kXcds - 1) / kXcds * kXcds;
-    const long long resident = 256 * (kLdsBytes / (long long)lds);
+    const long long resident = kCus * (kLdsBytes / (long long)lds);
     if (blocks > resident) blocks = resident;
     hipLaunchKernelGGL((moedisp_expert_gemm<BM, BN, WM, WN, WS, XS, FMT, F32>), dim3((unsigned)blocks),
                        dim3(T::kThreads), lds, stream, a);
@@ -355,7 +355,11 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
 //     192        -       393     377     371      464      299
 // Where the whole product is few tiles, the smallest spread it over the
 // device (24 experts of 125 rows, K = 640, N = 1000, fp32 results: 14.5 us
-// against 18.8 with 128 x 256).
+// against 18.8 with 128 x 256).  Many rows, but tiles of 256 x 256 in whole rounds
+// of one for each unit cover half as much again as those of 128 x 256 do: those
+// (12 experts of 206 rows, K = 2816, N = 2216: 30 us against 40; 15 of 784 rows,
+// K = 1408, N = 1200: 33 against 47; not 9 of 335 rows, K = 3584, N = 3536, with
+// 1.35 times as much: 61 against 52).
 template <int FMT, bool F32>
 hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
     const long long small = (long long)a.r.E * (((long long)mean_rows + 31) / 32) * ((a.n + 127) / 128);
@@ -367,6 +371,11 @@ hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t st
     } else {
         if (mean_rows <= 112) return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
         if (mean_rows <= 144) return launch_tile<160, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+        const long long nt = (a.n + 255) / 256;
+        const long long large = a.r.E * (((long long)mean_rows + 255) / 256) * nt;
+        const long long half = a.r.E * (((long long)mean_rows + 127) / 128) * nt;
+        const long long rounds = (large + kCus - 1) / kCus * kCus;
+        if (rounds * 4 > half * 3) return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
         return launch_tile<256, 256, 4, 2, 2, 2, FMT, F32>(a, stream);
     }
 }
