@@ -23,8 +23,8 @@
 // conflicts (weights that go to registers in operand order cost 4 times the
 // load time: 16 rows by 64 bytes do not coalesce).  The weights are the matrix
 // instruction's rows, the tokens its columns: a lane's four results then
-// belong to one token, whose scale is one factor.  Columns are dealt to the
-// instruction so that two results make 8 neighbours, one 16-byte store.
+// belong to one token, whose scale is one factor.  bf16 results' columns are dealt
+// to the instruction so that two of them make 8 neighbours, one 16-byte store.
 // Workgroups stay and take tile after tile; which expert a tile belongs to
 // comes from one scan over the experts' rows, so the host needs no counts.
 #include "experts_common.h"
@@ -353,9 +353,12 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
 //      96       362      249     255     217      239      285
 //     128        -       304     331     282      247      291
 //     192        -       393     377     371      464      299
-// Where the whole product is few tiles, the smallest spread it over the
-// device (24 experts of 125 rows, K = 640, N = 1000, fp32 results: 14.5 us
-// against 18.8 with 128 x 256).  Many rows, but tiles of 256 x 256 in whole rounds
+// Where the whole product is few tiles, small ones spread it over the device:
+// the smallest while they are resident at once (two to a unit), those of 64 x
+// 256 for as much again if experts fill more than half of them (33 experts of
+// 64 rows, K = 4096, N = 1656, fp32 results: 45 us against 59 with 32 x 128; 24
+// of 125 rows, K = 640, N = 1000, fp32 results: 14 us against 14.6, and 18.8
+// with 128 x 256).  Many rows, but tiles of 256 x 256 in whole rounds
 // of one for each unit cover half as much again as those of 128 x 256 do: those
 // (12 experts of 206 rows, K = 2816, N = 2216: 30 us against 40; 15 of 784 rows,
 // K = 1408, N = 1200: 33 against 47; not 9 of 335 rows, K = 3584, N = 3536, with
@@ -363,8 +366,9 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
 template <int FMT, bool F32>
 hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
     const long long small = (long long)a.r.E * (((long long)mean_rows + 31) / 32) * ((a.n + 127) / 128);
-    if (mean_rows <= 16 || small <= 1024) return launch_tile<32, 128, 1, 4, 3, 3, FMT, F32>(a, stream);
-    if (mean_rows <= 32) return launch_tile<64, 256, 2, 4, 3, 3, FMT, F32>(a, stream);
+    if (mean_rows <= 16 || small <= 2 * kCus || (mean_rows <= 32 && small <= 4 * kCus))
+        return launch_tile<32, 128, 1, 4, 3, 3, FMT, F32>(a, stream);
+    if (mean_rows <= 32 || small <= 4 * kCus) return launch_tile<64, 256, 2, 4, 3, 3, FMT, F32>(a, stream);
     if (mean_rows <= 72) return launch_tile<96, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
     if constexpr (F32) {  // larger tiles' widened operands leave the registers
         return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
