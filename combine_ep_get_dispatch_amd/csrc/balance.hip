@@ -376,11 +376,15 @@ __global__ __launch_bounds__(kBalThreads) void moedisp_balance_backward(BalanceA
     some = s_some[0] + s_some[1] + s_some[2] + s_some[3];
     const double n = a.tokens_per_seq[seq];
     const float scale = n > 0.0 ? (float)((double)a.coef * a.E * *a.d_loss / ((double)some * a.k * n * n)) : 0.0f;
+    // As the scores of a row add up to 1, the same may be taken from all counts:
+    // with their mean taken away what differs between them is not lost in
+    // w - dot where they are nearly equal.
+    const int mean = (int)((long long)n * a.k / a.E);
     float w[N];
 #pragma unroll
     for (int v = 0; v < N; ++v) {
         const int e = ((v >> 3) * LPR + l) * 8 + (v & 7);
-        w[v] = e < a.E ? scale * (float)a.tokens_per_expert[(size_t)seq * a.E + e] : 0.0f;
+        w[v] = e < a.E ? scale * (float)(a.tokens_per_expert[(size_t)seq * a.E + e] - mean) : 0.0f;
     }
     bool bad = false;
     for (int base = t0; base < t1; base += kRows) {

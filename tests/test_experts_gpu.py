@@ -541,6 +541,28 @@ def test_balance_bad_ids_and_empty():
 
 
 @pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("S,L,E,k", [(2, 64, 8, 8), (1, 4096, 64, 4), (3, 1600, 100, 5)])
+def test_balance_gradient_of_nearly_equal_counts(S, L, E, k, score):
+    """Experts in turn, so that all counts are equal: the gradient is exactly
+    zero; and with one slot masked, good to the size of what the counts differ
+    by, not of the counts."""
+    z, _ = balance_inputs(S, L, E, k, torch.float32, 34)
+    idx = ((torch.arange(L * k, device="cuda") % E).view(L, k).repeat(S, 1)).to(torch.int32).contiguous()
+    assert L * k % E == 0
+    h = Balance(S, L, E, k, score)
+    h.forward(z, idx)
+    assert (h.counts == L * k // E).all()
+    assert (h.backward(z, idx) == 0).all()
+    idx[5, 1] = -1
+    h.forward(z, idx)
+    dz = h.backward(z, idx)
+    _, _, _, want = balance64(z, idx, S, k, float(h.b.coef), score, 1.5)
+    # as in check_balance, with the counts' difference from their mean (at most 1) in the place of the counts
+    w = 1.5 * h.b.coef * E / (S * k * L ** 2)
+    within(dz, want, (2 * E + 40) * U * w * torch.ones_like(want), "d_logits")
+
+
+@pytest.mark.parametrize("score", SCORES)
 def test_balance_gradient_by_differences(score):
     """The loss is a function of the logits at fixed choices: central
     differences of the 64-bit loss against the kernel's gradient."""
