@@ -335,7 +335,7 @@ __global__ __launch_bounds__(kSeqThreads) void moedisp_balance_seq(BalanceArgs a
         // and acquire order would write back and drop a whole L2: 4 us.)
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const uint32_t before =
-            __hip_atomic_fetch_add(&a.hdr->reserved0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_fetch_add(&a.hdr->finished, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         s_last = before == gridDim.x - 1;
     }
     __syncthreads();
@@ -348,8 +348,9 @@ __global__ __launch_bounds__(kSeqThreads) void moedisp_balance_seq(BalanceArgs a
     sum = block_sum(sum, s_sum);
     some = block_sum(some, s_sum);
     if (tid == 0) {
+        if (a.S > 0) a.hdr->tables_lost = 1;  // the sums above lie where a split dispatch keeps its tables
         *a.loss = some > 0.0 ? (float)(a.coef * sum / some) : 0.0f;
-        __hip_atomic_store(&a.hdr->reserved0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+        __hip_atomic_store(&a.hdr->finished, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
     }
 }
 

@@ -112,7 +112,10 @@ static __device__ inline uint32_t offsets_scan(const DispatchArgs& a, int32_t* s
     bool bad = false;
     const long long total = block_exclusive_scan(a.tokens_per_expert, a.E, s, s_wave, &bad);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.expert_offsets[e] = s[e];
-    if (threadIdx.x == 0) a.expert_offsets[a.E] = (int32_t)total;
+    if (threadIdx.x == 0) {
+        a.expert_offsets[a.E] = (int32_t)total;
+        if (a.tables_lost) *a.tables_lost = 0;  // this launch writes them anew
+    }
     return (bad || total > a.capacity) ? (uint32_t)MOEDISP_DEV_BAD_LAYOUT : 0u;
 }
 
@@ -195,6 +198,7 @@ static __device__ inline void layout_reduce(const LayoutArgs& a, int32_t* s_tot,
     }
     if (tid == 0) {
         a.expert_offsets[a.E] = total;
+        a.hdr->tables_lost = 0;  // this call writes them anew
         if (total > a.capacity) atomicOr(&a.hdr->status, (uint32_t)MOEDISP_DEV_BAD_LAYOUT);
     }
 }

@@ -45,8 +45,9 @@ constexpr int kMaxBlockSlots = 512;        // >= kMaxBlockTokens * kMaxTopk
 // First 256 bytes of the workspace.
 struct WsHeader {
     uint32_t status;           // MOEDISP_DEV_* bits, or-ed by kernels
-    uint32_t reserved0;        // workgroups done (balance loss); zero between calls
-    uint32_t reserved[62];
+    uint32_t finished;         // workgroups done (balance loss); zero between calls
+    uint32_t tables_lost;      // 1: the balance loss wrote where a notify phase keeps its tables
+    uint32_t reserved[61];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
@@ -256,6 +257,9 @@ struct DispatchArgs {
     int32_t* recv_topk_idx;
     float* recv_topk_weights;
     WsHeader* hdr;
+    // the header's word of that name for the two phases of a split dispatch
+    // (notify clears it, scatter checks it), else nullptr
+    uint32_t* tables_lost;
     int32_t* tile_counts;
     // block-pull tables (pull.use != 0)
     PullPlan pull;

@@ -37,7 +37,9 @@
  *     handle) set bits of a status word in `ws`, read by ep_check_status.
  *     The library never asserts or aborts.
  *   - Calls that share one `ws` must be ordered on one stream; concurrent
- *     calls need distinct workspaces.
+ *     calls need distinct workspaces.  Nothing in `ws` but the status word
+ *     outlasts a call, with one exception: ep_dispatch_scatter reads what
+ *     ep_dispatch_notify left there (see both).
  */
 #ifndef MOEDISP_H
 #define MOEDISP_H
@@ -163,7 +165,10 @@ int ep_dispatch_noalloc(const moedisp_shape* shape, const void* x, const float* 
  *   and expert_offsets that ep_dispatch_notify left for the same topk_idx and
  *   tokens_per_expert in the same `ws` (stream-ordered before it, with no
  *   other dispatch-family call on that `ws` in between: those reuse the
- *   same workspace tables).
+ *   same workspace tables).  ep_balance_loss writes there too: on a `ws` of
+ *   its own, or before the notify phase or after the scatter, it may run; on
+ *   this `ws` between the two, ep_dispatch_scatter sets BAD_LAYOUT and its
+ *   outputs are not to be used.
  * Arguments, layouts and status bits as for ep_dispatch. */
 int ep_dispatch_notify(const moedisp_shape* shape, const int32_t* topk_idx, const int32_t* tokens_per_expert,
                        int32_t* expert_offsets, void* ws, size_t ws_bytes, void* stream);
@@ -498,7 +503,9 @@ size_t ep_balance_workspace_bytes(const moedisp_balance* b);
  *   topk_idx           int32 [S*L][k], -1 = masked.
  *   loss               fp32 [1];  tokens_per_expert int32 [S][E] = c;
  *   tokens_per_seq     int32 [S] = L_s.
- * Sums are binary32 and fixed in order.  Status bits: BAD_EXPERT_ID. */
+ * Sums are binary32 and fixed in order.  The whole of `ws` is written: it must
+ * not be the workspace of a split dispatch between its two phases
+ * (ep_dispatch_notify).  Status bits: BAD_EXPERT_ID. */
 int ep_balance_loss(const moedisp_balance* b, const void* logits, const int32_t* topk_idx, float* loss,
                     int32_t* tokens_per_expert, int32_t* tokens_per_seq, void* ws, size_t ws_bytes, void* stream);
 
