@@ -55,7 +55,7 @@ EXPORTS = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_dispatch_layout", 
            "ep_balance_workspace_bytes", "ep_balance_loss", "ep_balance_loss_backward")
 # tools (include/moedisp_tools.h): plan query and calibration probes, exported
 # by the same library
-CALIB_EXPORTS = ("ep_plan_query", "ep_probe_read", "ep_probe_copy", "ep_probe_fill")
+CALIB_EXPORTS = ("ep_plan_query", "ep_expert_plan_query", "ep_balance_plan_query", "ep_probe_read", "ep_probe_copy", "ep_probe_fill")
 
 
 class MoeDispError(RuntimeError):
@@ -104,6 +104,16 @@ class moedisp_balance(C.Structure):
     @classmethod
     def make(cls, num_seqs, seq_len, num_experts, topk, score=SCORE_SOFTMAX, logits_dtype=FP32, coef=1.0):
         return cls(num_seqs, seq_len, num_experts, topk, score, logits_dtype, coef)
+
+
+class moedisp_expert_plan_info(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("struct_bytes", "product_rows", "product_cols", "wgrad_cols",
+                                         "wgrad_channels", "swiglu_rows", "swiglu_blocks", "swiglu_backward_blocks")]
+
+
+class moedisp_balance_plan_info(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("struct_bytes", "tile_tokens", "tiles", "lanes", "rows_at_once", "passes",
+                                         "backward_blocks")]
 
 
 class moedisp_launch_info(C.Structure):
@@ -222,6 +232,10 @@ def load(path: str = LIB_PATH):
     L.ep_balance_loss_backward.restype = C.c_int
     L.ep_plan_query.argtypes = [S, C.POINTER(moedisp_plan_info), C.c_size_t]
     L.ep_plan_query.restype = C.c_int
+    L.ep_expert_plan_query.argtypes = [R, i32, i32, i32, i32, C.POINTER(moedisp_expert_plan_info), sz]
+    L.ep_expert_plan_query.restype = C.c_int
+    L.ep_balance_plan_query.argtypes = [Bl, C.POINTER(moedisp_balance_plan_info), sz]
+    L.ep_balance_plan_query.restype = C.c_int
     L.ep_probe_read.argtypes = [P, C.c_size_t, P, P]
     L.ep_probe_read.restype = C.c_int
     L.ep_probe_copy.argtypes = [P, P, C.c_size_t, P]
@@ -815,6 +829,21 @@ def ep_plan_query(shape) -> dict:
     (launches as nested dicts); raises for a shape the library rejects."""
     info = moedisp_plan_info()
     _check("ep_plan_query", load().ep_plan_query(C.byref(shape), C.byref(info), C.sizeof(info)))
+    return _as_dict(info)
+
+
+def ep_expert_plan_query(rows, n, k, scale_fmt, out_dtype) -> dict:
+    """Tiles of the experts' operators for these rows (no device touched)."""
+    info = moedisp_expert_plan_info()
+    _check("ep_expert_plan_query", load().ep_expert_plan_query(
+        C.byref(rows), int(n), int(k), int(scale_fmt), int(out_dtype), C.byref(info), C.sizeof(info)))
+    return _as_dict(info)
+
+
+def ep_balance_plan_query(balance) -> dict:
+    """How the balance loss cuts its batch (no device touched)."""
+    info = moedisp_balance_plan_info()
+    _check("ep_balance_plan_query", load().ep_balance_plan_query(C.byref(balance), C.byref(info), C.sizeof(info)))
     return _as_dict(info)
 
 

@@ -3,7 +3,9 @@
 // capi.hip, a rejected call touches no device and enqueues nothing.
 #include <math.h>
 #include <stddef.h>
+#include <string.h>
 
+#include "moedisp_tools.h"
 #include "experts_common.h"
 
 namespace moedisp {
@@ -287,6 +289,43 @@ int ep_balance_loss_backward(const moedisp_balance* b, const void* logits, const
     a.d_loss = d_loss;
     a.d_logits = d_logits;
     return status_of(launch_balance_backward(a, b->logits_dtype == MOEDISP_BF16, (hipStream_t)stream));
+}
+
+int ep_expert_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale_fmt, int32_t out_dtype,
+                         moedisp_expert_plan_info* info, size_t info_bytes) {
+    if (!info || info_bytes != sizeof(moedisp_expert_plan_info)) return MOEDISP_ERR_INVALID_ARG;
+    memset(info, 0, sizeof *info);
+    static const int32_t some_bounds = 0;  // the query has no bounds; the rows' own rules are checked
+    int st = check_rows(rows, &some_bounds);
+    if (st || (st = check_product(n, k, scale_fmt, out_dtype))) return st;
+    info->struct_bytes = (int64_t)sizeof *info;
+    const TileShape g = expert_gemm_tile(rows->num_experts, n, mean_rows(*rows), out_dtype == MOEDISP_FP32);
+    info->product_rows = g.a;
+    info->product_cols = g.b;
+    const TileShape w = expert_wgrad_tile(rows->num_experts, n, k);
+    info->wgrad_cols = w.a;
+    info->wgrad_channels = w.b;
+    const int blocks = k / kScaleBlock;
+    info->swiglu_rows = swiglu_rows_at_once(blocks);
+    info->swiglu_blocks = swiglu_blocks(rows->max_rows, blocks, false);
+    info->swiglu_backward_blocks = swiglu_blocks(rows->max_rows, blocks, true);
+    return MOEDISP_OK;
+}
+
+int ep_balance_plan_query(const moedisp_balance* b, moedisp_balance_plan_info* info, size_t info_bytes) {
+    if (!info || info_bytes != sizeof(moedisp_balance_plan_info)) return MOEDISP_ERR_INVALID_ARG;
+    memset(info, 0, sizeof *info);
+    const int st = check_balance(b);
+    if (st) return st;
+    info->struct_bytes = (int64_t)sizeof *info;
+    const BalancePlan p = plan_balance(*b);
+    info->tile_tokens = p.tile_tokens;
+    info->tiles = p.tiles;
+    info->lanes = balance_lanes(b->num_experts);
+    info->rows_at_once = 256 / info->lanes;
+    info->passes = p.tile_tokens / info->rows_at_once;
+    info->backward_blocks = (int64_t)b->num_seqs * p.tiles;
+    return MOEDISP_OK;
 }
 
 }  // extern "C"

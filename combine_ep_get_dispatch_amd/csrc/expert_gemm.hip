@@ -340,6 +340,21 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int FMT, bool F32>
+hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
+    const TileShape t = expert_gemm_tile(a.r.E, a.n, mean_rows, F32);
+    if (t.a == 32) return launch_tile<32, 128, 1, 4, 3, 3, FMT, F32>(a, stream);
+    if (t.a == 64) return launch_tile<64, 256, 2, 4, 3, 3, FMT, F32>(a, stream);
+    if (t.a == 96) return launch_tile<96, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+    if constexpr (!F32) {  // larger tiles' widened operands leave the registers
+        if (t.a == 160) return launch_tile<160, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+        if (t.a == 256) return launch_tile<256, 256, 4, 2, 2, 2, FMT, F32>(a, stream);
+    }
+    return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
+}
+
+}  // namespace
+
 // Tile by the rows an expert usually has.  Every weight is read once per row
 // tile, so the tile holds the rows of a usual expert with some to spare, and
 // is no higher: the rows' loads take LDS from the weights' that come from HBM
@@ -363,28 +378,20 @@ hipError_t launch_tile(ExpertGemmArgs a, hipStream_t stream) {
 // (12 experts of 206 rows, K = 2816, N = 2216: 30 us against 40; 15 of 784 rows,
 // K = 1408, N = 1200: 33 against 47; not 9 of 335 rows, K = 3584, N = 3536, with
 // 1.35 times as much: 61 against 52).
-template <int FMT, bool F32>
-hipError_t launch_variant(const ExpertGemmArgs& a, int mean_rows, hipStream_t stream) {
-    const long long small = (long long)a.r.E * (((long long)mean_rows + 31) / 32) * ((a.n + 127) / 128);
-    if (mean_rows <= 16 || small <= 2 * kCus || (mean_rows <= 32 && small <= 4 * kCus))
-        return launch_tile<32, 128, 1, 4, 3, 3, FMT, F32>(a, stream);
-    if (mean_rows <= 32 || small <= 4 * kCus) return launch_tile<64, 256, 2, 4, 3, 3, FMT, F32>(a, stream);
-    if (mean_rows <= 72) return launch_tile<96, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
-    if constexpr (F32) {  // larger tiles' widened operands leave the registers
-        return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
-    } else {
-        if (mean_rows <= 112) return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
-        if (mean_rows <= 144) return launch_tile<160, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
-        const long long nt = (a.n + 255) / 256;
-        const long long large = a.r.E * (((long long)mean_rows + 255) / 256) * nt;
-        const long long half = a.r.E * (((long long)mean_rows + 127) / 128) * nt;
-        const long long rounds = (large + kCus - 1) / kCus * kCus;
-        if (rounds * 4 > half * 3) return launch_tile<128, 256, 2, 4, 3, 2, FMT, F32>(a, stream);
-        return launch_tile<256, 256, 4, 2, 2, 2, FMT, F32>(a, stream);
-    }
+TileShape expert_gemm_tile(int E, int n, int mean_rows, bool f32_out) {
+    const long long small = (long long)E * (((long long)mean_rows + 31) / 32) * ((n + 127) / 128);
+    if (mean_rows <= 16 || small <= 2 * kCus || (mean_rows <= 32 && small <= 4 * kCus)) return {32, 128};
+    if (mean_rows <= 32 || small <= 4 * kCus) return {64, 256};
+    if (mean_rows <= 72) return {96, 256};
+    if (f32_out || mean_rows <= 112) return {128, 256};
+    if (mean_rows <= 144) return {160, 256};
+    const long long nt = (n + 255) / 256;
+    const long long large = E * (((long long)mean_rows + 255) / 256) * nt;
+    const long long half = E * (((long long)mean_rows + 127) / 128) * nt;
+    const long long rounds = (large + kCus - 1) / kCus * kCus;
+    if (rounds * 4 > half * 3) return {128, 256};
+    return {256, 256};
 }
-
-}  // namespace
 
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, int mean_rows, int scale_fmt, bool f32_out,
                               hipStream_t stream) {

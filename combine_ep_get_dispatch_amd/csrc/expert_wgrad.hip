@@ -290,20 +290,10 @@ hipError_t launch_one(ExpertWgradArgs a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Tiles of 256 x 256 move the fewest bytes per product (8 experts of 4096 x
-// 4096 and 4096 rows each: 1069 us against 1459 with 128 x 128).  Tiles of 128 x
-// 128 (two workgroups to a unit) where large ones, in whole rounds of one for
-// each unit, cover a fifth more than small ones do: 8 experts of 512 x 512 and
-// 1024 rows each 24 us against 47, 52 of 2008 x 128 26 against 33, 13 of 1048
-// x 3328 42 against 51; not 35 of 3264 x 1536 (1.03 times as much), 164 against
-// 179.
 template <int FMT, bool F32, bool ADD>
 hipError_t launch_tiles(const ExpertWgradArgs& a, hipStream_t stream) {
-    const long long large = (long long)a.r.E * ((a.n + 255) / 256) * ((a.k + 255) / 256);
-    const long long small = (long long)a.r.E * ((a.n + 127) / 128) * ((a.k + 127) / 128);
-    const long long rounds = (large + kCus - 1) / kCus * kCus;
-    return rounds * 4 * 5 <= small * 6 ? launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream)
-                                       : launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
+    return expert_wgrad_tile(a.r.E, a.n, a.k).a == 256 ? launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream)
+                                                       : launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
 }
 
 template <int FMT>
@@ -313,6 +303,20 @@ hipError_t launch_fmt(const ExpertWgradArgs& a, bool f32_out, bool accumulate, h
 }
 
 }  // namespace
+
+// Tiles of 256 x 256 move the fewest bytes per product (8 experts of 4096 x
+// 4096 and 4096 rows each: 1069 us against 1459 with 128 x 128).  Tiles of 128 x
+// 128 (two workgroups to a unit) where large ones, in whole rounds of one for
+// each unit, cover a fifth more than small ones do: 8 experts of 512 x 512 and
+// 1024 rows each 24 us against 47, 52 of 2008 x 128 26 against 33, 13 of 1048
+// x 3328 42 against 51; not 35 of 3264 x 1536 (1.03 times as much), 164 against
+// 179.
+TileShape expert_wgrad_tile(int E, int n, int k) {
+    const long long large = (long long)E * ((n + 255) / 256) * ((k + 255) / 256);
+    const long long small = (long long)E * ((n + 127) / 128) * ((k + 127) / 128);
+    const long long rounds = (large + kCus - 1) / kCus * kCus;
+    return rounds * 4 * 5 <= small * 6 ? TileShape{256, 256} : TileShape{128, 128};
+}
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, int scale_fmt, bool f32_out, bool accumulate,
                                hipStream_t stream) {

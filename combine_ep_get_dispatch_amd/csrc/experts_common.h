@@ -208,6 +208,15 @@ inline int balance_lanes(int E) {
     return lanes;
 }
 
+// Tile of rows by columns (product), of columns by channels (weight gradient).
+struct TileShape {
+    int a, b;
+};
+TileShape expert_gemm_tile(int E, int n, int mean_rows, bool f32_out);
+TileShape expert_wgrad_tile(int E, int n, int k);
+long long swiglu_rows_at_once(int blocks);
+long long swiglu_blocks(int max_rows, int blocks, bool backward);
+
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, int scale_fmt, bool f32_out, bool accumulate,
                                hipStream_t stream);
 hipError_t launch_swiglu(const SwigluArgs& a, int scale_fmt, hipStream_t stream);

@@ -175,10 +175,7 @@ __global__ __launch_bounds__(kSwigluThreads, BACKWARD ? 7 : 8) void moedisp_swig
 
 template <bool BACKWARD>
 hipError_t launch(const SwigluArgs& a, int scale_fmt, hipStream_t stream) {
-    const long long rows_at_once = a.blocks >= kUnits ? 1 : kUnits / a.blocks;
-    long long blocks = ((long long)a.r.max_rows + rows_at_once - 1) / rows_at_once;
-    if (blocks > 256 * (BACKWARD ? 7 : 8)) blocks = 256 * (BACKWARD ? 7 : 8);  // all resident at once
-    if (blocks < 1) blocks = 1;              // the bounds are checked even where no row can be
+    const long long blocks = swiglu_blocks(a.r.max_rows, a.blocks, BACKWARD);
     if (scale_fmt == MOEDISP_SCALE_UE8M0)
         hipLaunchKernelGGL((moedisp_swiglu<MOEDISP_SCALE_UE8M0, BACKWARD>), dim3((unsigned)blocks),
                            dim3(kSwigluThreads), 0, stream, a);
@@ -189,6 +186,15 @@ hipError_t launch(const SwigluArgs& a, int scale_fmt, hipStream_t stream) {
 }
 
 }  // namespace
+
+long long swiglu_rows_at_once(int blocks) { return blocks >= kUnits ? 1 : kUnits / blocks; }
+
+long long swiglu_blocks(int max_rows, int blocks, bool backward) {
+    const long long once = swiglu_rows_at_once(blocks);
+    const long long all = ((long long)max_rows + once - 1) / once;
+    const long long resident = (long long)kCus * (backward ? 7 : 8);
+    return all < 1 ? 1 : all < resident ? all : resident;  // the bounds are checked even where no row can be
+}
 
 hipError_t launch_swiglu(const SwigluArgs& a, int scale_fmt, hipStream_t stream) {
     return launch<false>(a, scale_fmt, stream);

@@ -16,7 +16,8 @@
  *
  * The plan query reports, for a shape, the launch geometry, LDS and
  * workspace layout the path's entry points would use, so that host-side
- * limits can be checked over many shapes without a GPU. */
+ * limits can be checked over many shapes without a GPU.  Two more report the
+ * tiles of the experts' operators and of the balance loss. */
 #ifndef MOEDISP_TOOLS_H
 #define MOEDISP_TOOLS_H
 
@@ -117,6 +118,35 @@ typedef struct moedisp_plan_info {
  * entry points reject; *info is then left zero), or INVALID_ARG when info is
  * NULL or info_bytes is not sizeof(moedisp_plan_info).  Touches no device. */
 int ep_plan_query(const moedisp_shape* shape, moedisp_plan_info* info, size_t info_bytes);
+
+/* Tiles of the experts' operators for one set of rows. */
+typedef struct moedisp_expert_plan_info {
+    int64_t struct_bytes;                       /* sizeof(moedisp_expert_plan_info) */
+    int64_t product_rows, product_cols;         /* ep_expert_gemm: rows by columns of y */
+    int64_t wgrad_cols, wgrad_channels;         /* ep_expert_wgrad: columns of dy by channels of x */
+    /* ep_swiglu_quant and ep_swiglu_backward of inner = k: rows that a
+     * workgroup takes at a time, and the workgroups */
+    int64_t swiglu_rows, swiglu_blocks, swiglu_backward_blocks;
+} moedisp_expert_plan_info;
+
+/* Fills *info for the calls of n columns, k channels and this scale format
+ * and result type.  Returns the calls' own code for arguments they reject
+ * (*info is then left zero), or INVALID_ARG when info is NULL or info_bytes is
+ * not its size.  Touches no device. */
+int ep_expert_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale_fmt, int32_t out_dtype,
+                         moedisp_expert_plan_info* info, size_t info_bytes);
+
+/* How ep_balance_loss and its backward pass cut a batch. */
+typedef struct moedisp_balance_plan_info {
+    int64_t struct_bytes;                /* sizeof(moedisp_balance_plan_info) */
+    int64_t tile_tokens, tiles;          /* tokens of a workgroup's tile, tiles of a sequence */
+    int64_t lanes, rows_at_once;         /* lanes that share a token's logits, tokens of a pass */
+    int64_t passes;                      /* passes of a full tile */
+    int64_t backward_blocks;             /* workgroups of the backward pass */
+} moedisp_balance_plan_info;
+
+/* As ep_expert_plan_query, for the shape of a balance loss. */
+int ep_balance_plan_query(const moedisp_balance* b, moedisp_balance_plan_info* info, size_t info_bytes);
 
 #ifdef __cplusplus
 }
