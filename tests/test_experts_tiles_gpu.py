@@ -7,7 +7,7 @@ import torch
 
 import combine_ep_get_dispatch_amd as M
 from experts_reference import E4M3, Problem
-from test_experts_gpu import FMTS, check_gemm
+from test_experts_gpu import FMTS, U, check_gemm, within
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,30 @@ def test_product_rows_do_not_depend_on_others(expected, tile, out):
     b = p.gemm(out)
     assert torch.equal(b[at - 5:at + 295], a[at:at + 300][perm])
     assert p.status() == 0
+
+
+# more than a round of tiles of 256 x 256, cut in both directions; rows round
+# the 32 of a step and the four stages
+WGRAD_ROWS = [(5 * e) % 7 for e in range(112)] + [0, 1, 31, 32, 33, 63, 64, 65, 95, 96, 97, 127, 128, 129, 161, 400]
+
+
+@pytest.mark.parametrize("out,accumulate", [(M.BF16, False), (M.FP32, False), (M.FP32, True)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_wgrad_256_tile(fmt, out, accumulate):
+    p = Problem(WGRAD_ROWS, 504, 640, fmt, seed=91)
+    assert_tile(p, out, wgrad=(256, 256))
+    before = torch.randn(p.E, 504, 640, device="cuda") if accumulate else None
+    dw = p.wgrad(out, accumulate, before.clone() if accumulate else None)
+    assert p.status() == 0
+    want, s = p.wgrad64()
+    if accumulate:
+        want, s = want + before.double(), s + before.abs().double()
+    rows = torch.tensor(WGRAD_ROWS, device="cuda").view(-1, 1, 1)
+    tol = (rows + 4) * U * s
+    if fmt == M.SCALE_FP32:
+        tol = tol + 2.0 ** -8 * s          # scale times code, rounded to bf16
+    if out == M.BF16:
+        tol = tol + 2.0 ** -8 * want.abs()
+    within(dw, want, tol)
+    if accumulate:
+        assert torch.equal(dw[0], before[0])  # an expert without rows
