@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import combine_ep_get_dispatch_amd as M
-from experts_reference import E4M3, Problem
-from test_experts_gpu import FMTS, U, check_gemm, within
+from experts_reference import E4M3, Problem, balance64, scales64, swiglu64, swiglu_backward64
+from test_experts_gpu import FMTS, SCORES, SWIGLU_REL, U, Balance, check_codes, check_gemm, within
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,105 @@ def test_wgrad_256_tile(fmt, out, accumulate):
     within(dw, want, tol)
     if accumulate:
         assert torch.equal(dw[0], before[0])  # an expert without rows
+
+
+# S, L, E, k: lanes that share a row from 1 to 64, rows of one to eight chunks
+# of the lanes, loads by 16 bytes and by element, more slots than lanes
+PASSES = [(64, 1013, 256, 8), (40, 1013, 257, 3), (60, 350, 600, 8), (50, 463, 1030, 32), (30, 703, 4096, 5),
+          (300, 4000, 5, 3), (33, 5000, 40, 12), (40, 8010, 24, 8), (1, 70001, 128, 8)]
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("S,L,E,k", PASSES)
+def test_balance_several_passes(S, L, E, k, score, dt):
+    """Tiles of three passes and more, the last tile of a sequence shorter;
+    padding tokens hold NaN beside live ones."""
+    h = Balance(S, L, E, k, score, dt)
+    plan = M.ep_balance_plan_query(h.b)
+    assert plan["passes"] >= 3 and L % plan["tile_tokens"] % plan["rows_at_once"] != 0, plan
+    g = torch.Generator(device="cuda").manual_seed(S + E)
+    z = (torch.randn(S * L, E, generator=g, device="cuda") * 2).to(dt)
+    idx = torch.rand(S * L, E, generator=g, device="cuda").topk(k, dim=1).indices.to(torch.int32)
+    idx[torch.rand(S * L, k, generator=g, device="cuda") < 0.1] = -1
+    idx[torch.rand(S * L, generator=g, device="cuda") < 0.2] = -1
+    pad = (idx < 0).all(1)
+    clean = z.clone()
+    z[pad], clean[pad] = float("nan"), 0.0
+    h.forward(z, idx)
+    dz = h.backward(z, idx)
+    assert M.ep_check_status(h.ws) == 0
+    loss, counts, tokens, want = balance64(clean, idx, S, k, float(h.b.coef), score, 1.5)
+    assert torch.equal(h.counts.long(), counts.long()) and torch.equal(h.tokens.long(), tokens)
+    within(h.loss, loss, (2 * E + L + 40) * U * loss.abs(), "loss")
+    n = tokens.double().clamp(min=1)
+    w = 1.5 * h.b.coef * E * counts.double() / ((tokens > 0).sum().clamp(min=1) * k * n[:, None] ** 2)
+    size = w.repeat_interleave(L, 0).amax(1, keepdim=True)
+    within(dz, want, (2 * E + 40) * U * size + (2.0 ** -8 * want.abs() if dt == torch.bfloat16 else 0), "d_logits")
+    assert (dz[pad] == 0).all()
+
+
+def swiglu_rows(inner, padded):
+    """Rows of four times what the workgroups take at once and some more, with
+    gaps: (problem of the rows, gate and up values, NaN in rows of no expert)."""
+    once = 2048 * max(1, 16 // (inner // 128))
+    if padded:
+        E, stride, cap = 37, 2 * once // 15, once // 9
+        p = Problem([(e * 997) % (cap + 50) for e in range(E)], 8, 128, M.SCALE_FP32, padded=(stride, cap, 5))
+    else:
+        p = Problem([once, 0, 3, once + 77, 2 * once], 8, 128, M.SCALE_FP32, spare=once // 3)
+    g = torch.Generator(device="cuda").manual_seed(inner)
+    gu = (torch.randn(p.R, 2 * inner, generator=g, device="cuda") * 2).to(torch.bfloat16)
+    gu[~p.live] = float("nan")
+    return p, gu
+
+
+SWIGLU = [(128, False), (128, True), (640, False), (640, True), (2048, False), (2176, True)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("inner,padded", SWIGLU)
+def test_swiglu_several_rows(inner, padded, fmt):
+    p, gu = swiglu_rows(inner, padded)
+    plan = M.ep_expert_plan_query(p.rows, 8, inner, fmt, M.BF16)
+    assert p.R > 4 * plan["swiglu_rows"] * plan["swiglu_blocks"]
+    h = torch.full((p.R, inner), 7, dtype=torch.uint8, device="cuda")
+    hs = torch.full((p.R, inner // 128), 7, device="cuda", dtype=torch.float32 if fmt == M.SCALE_FP32 else torch.uint8)
+    M.ep_swiglu_quant(p.rows, inner, fmt, gu, p.bounds, h, hs, p.ws)
+    assert p.status() == 0
+    check_codes(h.view(E4M3)[p.live], hs[p.live], swiglu64(gu[p.live]), SWIGLU_REL, "h")
+    assert (h[~p.live] == 7).all() and (hs[~p.live] == 7).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("inner,padded", SWIGLU)
+def test_swiglu_backward_several_rows(inner, padded, fmt):
+    p, gu = swiglu_rows(inner, padded)
+    plan = M.ep_expert_plan_query(p.rows, 8, inner, fmt, M.BF16)
+    assert p.R > 4 * plan["swiglu_rows"] * plan["swiglu_backward_blocks"]
+    live = p.live
+    g = torch.Generator(device="cuda").manual_seed(inner + 1)
+    dh = torch.randn(p.R, inner, generator=g, device="cuda").to(torch.bfloat16)
+    dh[~live] = float("nan")
+    dgu = torch.full((p.R, 2 * inner), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.full((p.R, 2 * inner), 7, dtype=torch.uint8, device="cuda")
+    qs = torch.full((p.R, inner // 64), 7, device="cuda", dtype=torch.float32 if fmt == M.SCALE_FP32 else torch.uint8)
+    M.ep_swiglu_backward(p.rows, inner, fmt, gu, dh, p.bounds, dgu, q, qs, p.ws)
+    assert p.status() == 0
+    assert (dgu[~live] == 7.0).all() and (q[~live] == 7).all() and (qs[~live] == 7).all()
+    want = swiglu_backward64(gu[live], dh[live])
+    gg, u = gu[live].double().chunk(2, -1)
+    s = torch.sigmoid(gg)
+    # dg has a factor 1 + g (1 - s) that can cancel: its error is relative to 1 + |g| (1 - s)
+    size = torch.cat([(dh[live].double() * u * s).abs() * (1 + gg.abs() * (1 - s)), want[:, inner:].abs()], -1)
+    own = 16 * 2.0 ** -23 * size
+    within(dgu[live], want, 2.0 ** -8 * want.abs() + own, "dgu")
+    real = scales64(qs[live])
+    b = want.view(want.shape[0], inner // 64, 128)
+    ob = own.view_as(b)
+    if fmt == M.SCALE_FP32:
+        amax = b.abs().amax(-1)
+        within(qs[live], amax / 448, ob.amax(-1) / 448 + 2.0 ** -23 * amax / 448, "scales")
+    got = q.view(E4M3)[live].double().view_as(b) * real[..., None]
+    tol = torch.maximum(2.0 ** -4 * b.abs(), 2.0 ** -10 * real[..., None]) * (1 + 2.0 ** -10) + 2 * ob
+    within(got, b, tol + 2.0 ** -20 * b.abs(), "codes")
