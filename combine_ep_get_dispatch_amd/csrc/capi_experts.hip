@@ -324,7 +324,7 @@ int ep_balance_plan_query(const moedisp_balance* b, moedisp_balance_plan_info* i
     info->lanes = balance_lanes(b->num_experts);
     info->rows_at_once = 256 / info->lanes;
     info->passes = p.tile_tokens / info->rows_at_once;
-    info->backward_blocks = (int64_t)b->num_seqs * p.tiles;
+    info->backward_blocks = balance_backward_blocks((long long)b->num_seqs * p.tiles);
     return MOEDISP_OK;
 }
 

@@ -217,6 +217,9 @@ TileShape expert_wgrad_tile(int E, int n, int k);
 long long swiglu_rows_at_once(int blocks);
 long long swiglu_blocks(int max_rows, int blocks, bool backward);
 
+// Workgroups of the balance loss's backward pass over so many tiles.
+inline long long balance_backward_blocks(long long tiles) { return tiles <= 4096 ? tiles : 2048; }
+
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, int scale_fmt, bool f32_out, bool accumulate,
                                hipStream_t stream);
 hipError_t launch_swiglu(const SwigluArgs& a, int scale_fmt, hipStream_t stream);

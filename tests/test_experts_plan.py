@@ -58,3 +58,11 @@ def test_refusals():
     assert L.ep_expert_plan_query(C.byref(rows), 8, 128, 0, 0, C.byref(info), 8) == B.ERR_INVALID_ARG
     b = M.moedisp_balance.make(1, 1, 4, 1)
     assert L.ep_balance_plan_query(C.byref(b), None, 56) == B.ERR_INVALID_ARG
+
+
+def test_backward_reads_of_the_token_counts():
+    """Every workgroup of the backward pass reads all S token counts: their
+    number does not grow with S, so neither do the reads of a sequence."""
+    for S, L in ((1, 1), (300, 2), (2048, 7), (4096, 1), (4097, 1), (65536, 16), (1 << 20, 1)):
+        p = M.ep_balance_plan_query(M.moedisp_balance.make(S, L, 64, 2))
+        assert p["backward_blocks"] <= min(4096, S * p["tiles"])

@@ -188,3 +188,40 @@ def test_swiglu_backward_several_rows(inner, padded, fmt):
     got = q.view(E4M3)[live].double().view_as(b) * real[..., None]
     tol = torch.maximum(2.0 ** -4 * b.abs(), 2.0 ** -10 * real[..., None]) * (1 + 2.0 ** -10) + 2 * ob
     within(got, b, tol + 2.0 ** -20 * b.abs(), "codes")
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("S,L,E,k", [(4097, 3, 16, 2), (5000, 40, 33, 3), (100003, 1, 8, 2), (4500, 2, 300, 4)])
+def test_balance_many_sequences(S, L, E, k, score, dt):
+    """More sequences than the backward pass has workgroups; some of them hold
+    padding alone."""
+    h = Balance(S, L, E, k, score, dt)
+    assert M.ep_balance_plan_query(h.b)["backward_blocks"] < S
+    g = torch.Generator(device="cuda").manual_seed(S)
+    z = (torch.randn(S * L, E, generator=g, device="cuda") * 2).to(dt)
+    idx = torch.rand(S * L, E, generator=g, device="cuda").topk(k, dim=1).indices.to(torch.int32)
+    idx[torch.rand(S * L, generator=g, device="cuda") < 0.3] = -1
+    idx.view(S, L, k)[torch.rand(S, generator=g, device="cuda") < 0.2] = -1
+    h.forward(z, idx)
+    dz = h.backward(z, idx)
+    assert M.ep_check_status(h.ws) == 0
+    # the definition in 64 bits (counts by one sum over all sequences)
+    z64 = z.double().view(S, L, E)
+    sg = torch.sigmoid(z64)
+    p = torch.softmax(z64, -1) if score == M.SCORE_SOFTMAX else sg / sg.sum(-1, keepdim=True)
+    live = (idx >= 0).any(1).view(S, L)
+    at = torch.where(idx < 0, E, idx).long().view(S, L * k)
+    counts = torch.zeros(S, E + 1, dtype=torch.int64, device="cuda").scatter_add_(1, at, torch.ones_like(at))[:, :E]
+    tokens = live.sum(1)
+    n, some = tokens.double().clamp(min=1)[:, None], int((tokens > 0).sum())
+    assert 0 < some < S and torch.equal(h.counts.long(), counts) and torch.equal(h.tokens.long(), tokens)
+    w = float(h.b.coef) * E * counts.double() / (some * k * n ** 2)
+    loss = (w * (p * live[..., None]).sum(1)).sum()
+    within(h.loss, loss, (2 * E + L + 40) * U * loss.abs(), "loss")
+    w = 1.5 * w[:, None, :]
+    want = p * (w - (p * w).sum(-1, keepdim=True)) * live[..., None]
+    if score == M.SCORE_SIGMOID:
+        want = want * (1 - sg)
+    tol = (2 * E + 40) * U * w.amax(-1, keepdim=True).expand_as(want)
+    within(dz.view(S, L, E), want, tol + (2.0 ** -8 * want.abs() if dt == torch.bfloat16 else 0), "d_logits")
