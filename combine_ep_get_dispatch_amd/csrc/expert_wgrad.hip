@@ -44,24 +44,32 @@ __device__ inline v4s read_transposed(const char* p) {
 // see into: with the builtin it waits for every load into LDS before a
 // transposing read, and nothing could be loaded ahead (1372 us against 1182
 // for 4096 x 4096 weights and 32768 rows).  There is no result register; the
-// waits are wait_loads_and_sync's and wait_own_loads'.  The leading s_nop
-// covers a descriptor that a vector instruction has just written.
+// waits are wait_loads_and_sync's and wait_own_loads'.  What stands before
+// the load covers a descriptor that a vector instruction has just written
+// (five wait states).
 template <int SIZE>
 __device__ inline void load_to_lds_unseen(const void* base, const char* lds, int voff) {
     const uint32_t to = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds;
     const v4i rs = {__builtin_amdgcn_readfirstlane((int)(uintptr_t)base),
                     __builtin_amdgcn_readfirstlane((int)((uintptr_t)base >> 32) & 0xFFFF), 0x7FFFFFFF, kRawBufferWord3};
+    int m0;  // put back: m0 is the compiler's, which takes no note of a clobber of it
     if constexpr (SIZE == 16)
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
-                     "v"(voff), "s"(rs)
+        asm volatile("s_mov_b32 %0, m0\n\ts_nop 2\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "s"(to), "v"(voff), "s"(rs)
                      : "memory");
     else if constexpr (SIZE == 4)
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
-                     "v"(voff), "s"(rs)
+        asm volatile("s_mov_b32 %0, m0\n\ts_nop 2\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "buffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "s"(to), "v"(voff), "s"(rs)
                      : "memory");
     else
-        asm volatile("s_nop 4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(to),
-                     "v"(voff), "s"(rs)
+        asm volatile("s_mov_b32 %0, m0\n\ts_nop 2\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                     "buffer_load_ubyte %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "s"(to), "v"(voff), "s"(rs)
                      : "memory");
 }
 
