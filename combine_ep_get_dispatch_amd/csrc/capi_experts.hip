@@ -302,7 +302,7 @@ int ep_expert_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, int32_t
     const TileShape g = expert_gemm_tile(rows->num_experts, n, mean_rows(*rows), out_dtype == MOEDISP_FP32);
     info->product_rows = g.a;
     info->product_cols = g.b;
-    const TileShape w = expert_wgrad_tile(rows->num_experts, n, k);
+    const TileShape w = expert_wgrad_tile(rows->num_experts, n, k, scale_fmt, out_dtype == MOEDISP_FP32);
     info->wgrad_cols = w.a;
     info->wgrad_channels = w.b;
     const int blocks = k / kScaleBlock;

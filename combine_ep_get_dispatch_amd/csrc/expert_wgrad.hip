@@ -3,12 +3,16 @@
 //
 // Precision.  The scales belong to rows, over which is summed, so they cannot
 // wait until after a matrix instruction: x becomes bf16, scale times code
-// rounded once (2^-8; exact for powers of two), and the products are those of
-// the bf16 instruction, added in binary32.
+// rounded once (by 2^-9 of itself at most; exact for powers of two), and the products are
+// those of the bf16 instruction, added in binary32.  bf16 results, rounded as
+// much themselves, take that.  fp32 results of FP32 scales are to keep
+// binary32's error, over micro-batches too: x becomes a sum of three bf16
+// terms, exact to binary32, and each has its product.
 //
 // What bounds it.  Many rows (32768 over 8 experts, 4096 x 4096): 1.07 ms, 1.0
 // PFLOP/s; products alone 0.78 ms, loads and LDS alone 0.91 ms.  Few rows (8192
 // over 64 experts, 7168 x 2048, fp32): the 3.8 GB of results, 0.94 ms, 4.1 TB/s.
+// Three terms: the products, 3.29 and 1.64 ms at these sizes.
 //
 // How.  A workgroup computes one tile over all rows of its expert, 32 rows a
 // step, three steps of loads under way.  Both operands are contracted over
@@ -73,14 +77,37 @@ __device__ inline void load_to_lds_unseen(const void* base, const char* lds, int
                      : "memory");
 }
 
+// Terms of scale times code: one, but three for fp32 results of FP32 scales.
+constexpr int wgrad_terms(int fmt, bool f32) { return fmt == MOEDISP_SCALE_FP32 && f32 ? 3 : 1; }
+
+// Two values as pairs of bf16: rounded once, or as a sum of three terms of
+// eight bits each, cut off one after the other, so that every step is exact and
+// the terms hold binary32's 24 bits.
+template <int TERMS>
+__device__ inline void bf16_terms(float v0, float v1, uint32_t o[TERMS]) {
+    if constexpr (TERMS == 1) {
+        o[0] = pack_bf16x2(v0, v1);
+    } else {
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+            const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
+            o[t] = (b0 >> 16) | (b1 & 0xFFFF0000u);
+            // infinity and NaN are their first term alone
+            v0 = t > 0 || fabsf(v0) < INFINITY ? v0 - __uint_as_float(b0 & 0xFFFF0000u) : 0.0f;
+            v1 = t > 0 || fabsf(v1) < INFINITY ? v1 - __uint_as_float(b1 & 0xFFFF0000u) : 0.0f;
+        }
+    }
+}
+
 // At most N of the wave's own loads are under way.
 template <int N>
 __device__ inline void wait_own_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Tile of TN columns of dy by TK channels of x; WN x WK waves.
-template <int TN, int TK, int WN, int WK>
+// Tile of TN columns of dy by TK channels of x; WN x WK waves; x as a sum of
+// TERMS bf16 values.
+template <int TN, int TK, int WN, int WK, int TERMS>
 struct WTile {
     static constexpr int kWaves = WN * WK;
     static constexpr int kThreads = 64 * kWaves;
@@ -95,13 +122,14 @@ struct WTile {
     static constexpr int kXRows = 64 / kXLanes;                // rows of a wave and step
     static constexpr int kOps = kDyLoads + 2;                  // loads of a wave and step
     static constexpr int kXRaw = 1024 + 256;                   // a wave's codes and scales of a step
-    static constexpr int kLds = kStages * (kDyStage + kWaves * kXRaw) + 2 * kXStage;
+    static constexpr int kLds = kStages * (kDyStage + kWaves * kXRaw) + 2 * TERMS * kXStage;
     static_assert(kKT >= 4 && kKT % 2 == 0 && kXRows * kWaves == kStep && kDyRow >= 256 && kXRow >= 256, "tile shape");
 };
 
 template <int TN, int TK, int WN, int WK, int FMT, bool F32, bool ADD>
 __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgradArgs a) {
-    using T = WTile<TN, TK, WN, WK>;
+    constexpr int TERMS = wgrad_terms(FMT, F32);
+    using T = WTile<TN, TK, WN, WK, TERMS>;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -156,7 +184,7 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
     // wave's own; from there they become bf16 (scale times code, rounded
     // once), zero past the expert's last row
     constexpr int SB = FMT == MOEDISP_SCALE_FP32 ? 4 : 1;
-    char* const raw = lds + kStages * T::kDyStage + 2 * T::kXStage + wave * (kStages * T::kXRaw);
+    char* const raw = lds + kStages * T::kDyStage + 2 * TERMS * T::kXStage + wave * (kStages * T::kXRaw);
     const int x_row = wave * T::kXRows + lane / T::kXLanes;
     const int x_ch = min(k0 + lane % T::kXLanes * 16, a.k - 16);
     auto load_x = [&](int step, int u) {
@@ -181,22 +209,31 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
         const int xs = *reinterpret_cast<const int*>(raw + u * T::kXRaw + 1024 + lane * 4);
         const float s = FMT == MOEDISP_SCALE_FP32 ? __int_as_float(xs) : ue8m0_value((uint32_t)xs);
         const uint32_t on = step * kStep + x_row < rows ? 0xFFFFFFFFu : 0u;
-        v4u o[2];
+        v4u o[TERMS][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], false);
             const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], true);
-            o[i >> 1][2 * (i & 1)] = pack_bf16x2(lo.x * s, lo.y * s) & on;
-            o[i >> 1][2 * (i & 1) + 1] = pack_bf16x2(hi.x * s, hi.y * s) & on;
+            uint32_t a[TERMS], b[TERMS];
+            bf16_terms<TERMS>(lo.x * s, lo.y * s, a);
+            bf16_terms<TERMS>(hi.x * s, hi.y * s, b);
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) {
+                o[t][i >> 1][2 * (i & 1)] = a[t] & on;
+                o[t][i >> 1][2 * (i & 1) + 1] = b[t] & on;
+            }
         }
         if (kPairs) {
-            const v4u t = {o[0][0], o[0][1], o[1][0], o[1][1]};
-            o[1] = v4u{o[0][2], o[0][3], o[1][2], o[1][3]};
-            o[0] = t;
+            const v4u t = {o[0][0][0], o[0][0][1], o[0][1][0], o[0][1][1]};
+            o[0][1] = v4u{o[0][0][2], o[0][0][3], o[0][1][2], o[0][1][3]};
+            o[0][0] = t;
         }
-        char* to = x_lds + (step & 1) * T::kXStage;
-        *reinterpret_cast<v4u*>(to + (x_half ? x_at[1] : x_at[0])) = x_half ? o[1] : o[0];
-        *reinterpret_cast<v4u*>(to + (x_half ? x_at[0] : x_at[1])) = x_half ? o[0] : o[1];
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+            char* to = x_lds + ((step & 1) * TERMS + t) * T::kXStage;
+            *reinterpret_cast<v4u*>(to + (x_half ? x_at[1] : x_at[0])) = x_half ? o[t][1] : o[t][0];
+            *reinterpret_cast<v4u*>(to + (x_half ? x_at[0] : x_at[1])) = x_half ? o[t][0] : o[t][1];
+        }
     };
 
     const int wk = wave % WK * (TK / WK), wn = wave / WK * (TN / WN);
@@ -232,17 +269,24 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
                 const int s = s0 + h;
                 if (s >= steps) break;
                 const char* ds = lds + h * T::kDyStage;
-                const char* xst = x_lds + (h & 1) * T::kXStage;
-                v8bf b[T::kNT], av[2];
+                const char* xst = x_lds + (h & 1) * TERMS * T::kXStage;
+                v8bf b[T::kNT], av[2][TERMS];
 #pragma unroll
                 for (int j = 0; j < T::kNT; ++j) b[j] = operand(ds, T::kDyRow, wn / 16 + j);
-                av[0] = operand(xst, T::kXRow, wk / 16);
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) av[0][t] = operand(xst + t * T::kXStage, T::kXRow, wk / 16);
 #pragma unroll
                 for (int i = 0; i < T::kKT; ++i) {
-                    if (i + 1 < T::kKT) av[(i + 1) & 1] = operand(xst, T::kXRow, wk / 16 + i + 1);
+                    if (i + 1 < T::kKT) {
 #pragma unroll
-                    for (int j = 0; j < T::kNT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1], b[j], acc[i][j], 0, 0, 0);
+                        for (int t = 0; t < TERMS; ++t)
+                            av[(i + 1) & 1][t] = operand(xst + t * T::kXStage, T::kXRow, wk / 16 + i + 1);
+                    }
+#pragma unroll
+                    for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+                        for (int j = 0; j < T::kNT; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1][t], b[j], acc[i][j], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                     // behind the products: step s + 3 into the place of step
                     // s - 1, which all waves have read; x of step s + 1
@@ -288,7 +332,7 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
 
 template <int TN, int TK, int WN, int WK, int FMT, bool F32, bool ADD>
 hipError_t launch_one(ExpertWgradArgs a, hipStream_t stream) {
-    using T = WTile<TN, TK, WN, WK>;
+    using T = WTile<TN, TK, WN, WK, wgrad_terms(FMT, F32)>;
     a.nt = (a.n + TN - 1) / TN;
     a.kt = (a.k + TK - 1) / TK;
     const long long blocks = ((long long)a.r.E * a.nt * a.kt + 255) / 256 * 256;  // whole runs of 32 on each XCD
@@ -300,8 +344,13 @@ hipError_t launch_one(ExpertWgradArgs a, hipStream_t stream) {
 
 template <int FMT, bool F32, bool ADD>
 hipError_t launch_tiles(const ExpertWgradArgs& a, hipStream_t stream) {
-    return expert_wgrad_tile(a.r.E, a.n, a.k).a == 256 ? launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream)
-                                                       : launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
+    const bool large = expert_wgrad_tile(a.r.E, a.n, a.k, FMT, F32).a == 256;
+    if constexpr (wgrad_terms(FMT, F32) == 1) {
+        if (large) return launch_one<256, 256, 4, 2, FMT, F32, ADD>(a, stream);
+    } else {
+        if (large) return launch_one<256, 128, 2, 2, FMT, F32, ADD>(a, stream);
+    }
+    return launch_one<128, 128, 2, 2, FMT, F32, ADD>(a, stream);
 }
 
 template <int FMT>
@@ -319,9 +368,19 @@ hipError_t launch_fmt(const ExpertWgradArgs& a, bool f32_out, bool accumulate, h
 // 1024 rows each 24 us against 47, 52 of 2008 x 128 26 against 33, 13 of 1048
 // x 3328 42 against 51; not 35 of 3264 x 1536 (1.03 times as much), 164 against
 // 179.
-TileShape expert_wgrad_tile(int E, int n, int k) {
-    const long long large = (long long)E * ((n + 255) / 256) * ((k + 255) / 256);
+//
+// Three terms of x leave LDS no room for 256 x 256, and for one workgroup to a
+// unit at either tile: 256 x 128, which a round of takes 1.4 times as long as one
+// of 128 x 128, unless the rounds are as many (fp32 results of FP32 scales, 8
+// experts of 4096 x 4096 and 4096 rows each: 3.29 ms against 4.75; 24 of 1000 x 640,
+// 88 rows: 43 us against 50; but 8 of 512 x 512 and 1024 rows: 65 us against 48).
+TileShape expert_wgrad_tile(int E, int n, int k, int scale_fmt, bool f32_out) {
     const long long small = (long long)E * ((n + 127) / 128) * ((k + 127) / 128);
+    if (wgrad_terms(scale_fmt, f32_out) > 1) {
+        const long long half = (long long)E * ((n + 255) / 256) * ((k + 127) / 128);
+        return (half + kCus - 1) / kCus * 7 <= (small + kCus - 1) / kCus * 5 ? TileShape{256, 128} : TileShape{128, 128};
+    }
+    const long long large = (long long)E * ((n + 255) / 256) * ((k + 255) / 256);
     const long long rounds = (large + kCus - 1) / kCus * kCus;
     return rounds * 4 * 5 <= small * 6 ? TileShape{256, 256} : TileShape{128, 128};
 }

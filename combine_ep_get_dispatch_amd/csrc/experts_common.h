@@ -213,7 +213,7 @@ struct TileShape {
     int a, b;
 };
 TileShape expert_gemm_tile(int E, int n, int mean_rows, bool f32_out);
-TileShape expert_wgrad_tile(int E, int n, int k);
+TileShape expert_wgrad_tile(int E, int n, int k, int scale_fmt, bool f32_out);
 long long swiglu_rows_at_once(int blocks);
 long long swiglu_blocks(int max_rows, int blocks, bool backward);
 

@@ -33,6 +33,11 @@ def test_wgrad_tiles():
     assert tile(8, 512, 512) == (128, 128) and tile(52, 2008, 128) == (128, 128)
     assert tile(35, 3264, 1536) == (256, 256) and tile(13, 1048, 3328) == (128, 128)
 
+    def exact(E, n, k):
+        p = M.ep_expert_plan_query(M.moedisp_rows.contiguous(E, 64), n, k, M.SCALE_FP32, M.FP32)
+        return p["wgrad_cols"], p["wgrad_channels"]
+    assert exact(8, 4096, 4096) == exact(24, 1000, 640) == (256, 128) and exact(8, 512, 512) == (128, 128)
+
 
 def test_balance_tiles():
     for S, L, E, k in ((64, 2048, 256, 8), (4, 1024, 256, 8), (1, 1, 1, 1), (3, 5000, 4096, 32), (70000, 2, 8, 1)):

@@ -70,7 +70,8 @@ WGRAD_ROWS = [(5 * e) % 7 for e in range(112)] + [0, 1, 31, 32, 33, 63, 64, 65, 
 @pytest.mark.parametrize("fmt", FMTS)
 def test_wgrad_256_tile(fmt, out, accumulate):
     p = Problem(WGRAD_ROWS, 504, 640, fmt, seed=91)
-    assert_tile(p, out, wgrad=(256, 256))
+    # fp32 results of FP32 scales take more of LDS, and a smaller tile
+    assert_tile(p, out, wgrad=(256, 128) if fmt == M.SCALE_FP32 and out == M.FP32 else (256, 256))
     before = torch.randn(p.E, 504, 640, device="cuda") if accumulate else None
     dw = p.wgrad(out, accumulate, before.clone() if accumulate else None)
     assert p.status() == 0
