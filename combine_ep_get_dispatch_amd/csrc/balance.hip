@@ -54,6 +54,13 @@ __device__ inline float lanes_max(float v) {
     return row_reduce<LPR>(v, [](float x, float y) { return fmaxf(x, y); });
 }
 
+template <int LPR>
+__device__ inline int lanes_sum(int v) {
+    return __float_as_int(row_reduce<LPR>(__int_as_float(v), [](float x, float y) {
+        return __int_as_float(__float_as_int(x) + __float_as_int(y));
+    }));
+}
+
 // Whether any of the row's LPR lanes has it.
 template <int LPR>
 __device__ inline bool lanes_any(bool v) {
@@ -393,14 +400,20 @@ __global__ __launch_bounds__(kBalThreads) void moedisp_balance_backward(BalanceA
         const float scale = n > 0.0 ? (float)((double)a.coef * a.E * *a.d_loss / ((double)some * a.k * n * n)) : 0.0f;
         // As the scores of a row add up to 1, the same may be taken from all counts:
         // with their mean taken away what differs between them is not lost in
-        // w - dot where they are nearly equal.
-        const int mean = (int)((long long)n * a.k / a.E);
-        float w[N];
+        // w - dot where they are nearly equal.  (Their own mean: masked slots are
+        // not counted.)
+        int c[N], slots = 0;
 #pragma unroll
         for (int v = 0; v < N; ++v) {
             const int e = ((v >> 3) * LPR + l) * 8 + (v & 7);
-            w[v] = e < a.E ? scale * (float)(a.tokens_per_expert[(size_t)seq * a.E + e] - mean) : 0.0f;
+            c[v] = e < a.E ? a.tokens_per_expert[(size_t)seq * a.E + e] : 0;
+            slots += c[v];
         }
+        const int mean = lanes_sum<LPR>(slots) / a.E;
+        float w[N];
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+            w[v] = ((v >> 3) * LPR + l) * 8 + (v & 7) < a.E ? scale * (float)(c[v] - mean) : 0.0f;
         bool bad = false;
         for (int base = t0; base < t1; base += kRows) {
             const int t = base + r;

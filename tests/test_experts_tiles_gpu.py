@@ -7,7 +7,7 @@ import torch
 
 import combine_ep_get_dispatch_amd as M
 from experts_reference import E4M3, Problem, balance64, scales64, swiglu64, swiglu_backward64
-from test_experts_gpu import FMTS, SCORES, SWIGLU_REL, U, Balance, check_codes, check_gemm, within
+from test_experts_gpu import (FMTS, SCORES, SWIGLU_REL, U, Balance, balance_inputs, check_codes, check_gemm, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -226,3 +226,26 @@ def test_balance_many_sequences(S, L, E, k, score, dt):
         want = want * (1 - sg)
     tol = (2 * E + 40) * U * w.amax(-1, keepdim=True).expand_as(want)
     within(dz.view(S, L, E), want, tol + (2.0 ** -8 * want.abs() if dt == torch.bfloat16 else 0), "d_logits")
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("S,L,E,k", [(2, 64, 8, 8), (1, 4096, 64, 4), (3, 1600, 100, 5), (1, 1200, 600, 4)])
+def test_balance_gradient_of_equal_counts_with_masked_slots(S, L, E, k, score):
+    """Every second slot masked, experts in turn in the others: the counts are
+    equal, the gradient exactly zero; one more slot masked, and it is good to
+    the size of what the counts differ by, not of the counts."""
+    z, _ = balance_inputs(S, L, E, k, torch.float32, 35)
+    at = torch.arange(L * k, device="cuda").view(L, k)
+    idx = torch.where(at % 2 == 0, (at // 2) % E, -1).repeat(S, 1).to(torch.int32).contiguous()
+    assert L * k // 2 % E == 0
+    h = Balance(S, L, E, k, score)
+    h.forward(z, idx)
+    assert (h.counts == L * k // 2 // E).all() and (h.tokens == L).all()
+    assert (h.backward(z, idx) == 0).all()
+    idx[3][idx[3] >= 0] = torch.where(torch.arange(int((idx[3] >= 0).sum()), device="cuda") == 0, -1, idx[3][idx[3] >= 0]).int()
+    h.forward(z, idx)
+    dz = h.backward(z, idx)
+    _, _, tokens, want = balance64(z, idx, S, k, float(h.b.coef), score, 1.5)
+    # as in check_balance, with the counts' difference from their mean (at most 1) in the place of the counts
+    w = 1.5 * h.b.coef * E / (S * k * float(tokens.min()) ** 2)
+    within(dz, want, (2 * E + 40) * U * w * torch.ones_like(want), "d_logits")
