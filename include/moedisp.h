@@ -410,7 +410,7 @@ typedef struct {
  * accumulated in binary32, rounded once to out_dtype.  fp32 results keep the
  * products and sums of a block to binary32; for bf16 results a block's sum
  * comes from the E4M3 matrix instruction, which keeps about 16 bits below the
- * largest products it adds (1.5e-5 of a result of normal rows, against the
+ * largest products it adds (1.4e-5 of a result of normal rows, against the
  * 2e-3 of its rounding to bf16).
  *   n          columns of y, n % 8 == 0, in [8, 2^20]; the last scale block
  *              may be cut.
@@ -447,14 +447,14 @@ int ep_expert_wgrad(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scal
 
 /* Gated activation with quantisation, between the two products of an expert:
  *   h[i] = silu(g[i]) * u[i] for gu's row (g[0..inner), u[0..inner)),
- *   silu(v) = v / (1 + exp(-v)), computed in binary32 (zero for v < -87) and
+ *   silu(v) = v / (1 + exp(-v)), computed in binary32 (zero for finite v < -87) and
  * quantised per block of 128 as ep_dispatch_quant does (scale_fmt FP32 or
  * UE8M0; the quotient h / scale is good to two steps of binary32).
  *   inner     inner % 128 == 0, in [128, 65536].
  *   gu        bf16 [max_rows][2*inner];  h E4M3 [max_rows][inner];
  *   h_scales  [max_rows][inner/128] float or uint8.
- * A block whose largest |h| is infinite or that holds NaN gets NaN codes
- * (0x7F), with the scale 1.  Status bits: BAD_LAYOUT. */
+ * A block whose largest |h| is infinite or that holds NaN (as from an infinite
+ * g) gets NaN codes (0x7F), with the scale 1.  Status bits: BAD_LAYOUT. */
 int ep_swiglu_quant(const moedisp_rows* rows, int32_t inner, int32_t scale_fmt, const void* gu,
                     const int32_t* row_bounds, void* h, void* h_scales, void* ws, size_t ws_bytes, void* stream);
 
@@ -465,7 +465,8 @@ int ep_swiglu_quant(const moedisp_rows* rows, int32_t inner, int32_t scale_fmt, 
  *   dgu_q, dgu_scales  the same gradient before rounding to bf16, quantised
  *                 as above: E4M3 [max_rows][2*inner] and
  *                 [max_rows][2*inner/128]; both NULL or both given.
- * At least one of the two forms is written.  Other arguments as above. */
+ * At least one of the two forms is written.  An infinite g gives NaN.  Other
+ * arguments as above. */
 int ep_swiglu_backward(const moedisp_rows* rows, int32_t inner, int32_t scale_fmt, const void* gu, const void* dh,
                        const int32_t* row_bounds, void* dgu, void* dgu_q, void* dgu_scales, void* ws,
                        size_t ws_bytes, void* stream);
@@ -500,8 +501,9 @@ size_t ep_balance_workspace_bytes(const moedisp_balance* b);
  *   loss = coef / S' * sum_s sum_e (E * c[s][e] / (k * L_s)) * (1/L_s * sum_t p[t][e])
  * (0 if S' is 0).
  *   logits             [S*L][E] bf16 or fp32, 16-byte aligned; -inf scores 0.
- *                      A row without a finite logit has p = 0 for all experts.  Rows of padding
- *                      tokens are not used, whatever they hold.
+ *                      A row of -inf alone has p = 0 for all experts; NaN and, for softmax,
+ *                      +inf make the loss NaN.  Rows of padding tokens are not used, whatever
+ *                      they hold.
  *   topk_idx           int32 [S*L][k], -1 = masked.
  *   loss               fp32 [1];  tokens_per_expert int32 [S][E] = c;
  *   tokens_per_seq     int32 [S] = L_s.
