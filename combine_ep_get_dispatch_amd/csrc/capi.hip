@@ -538,7 +538,6 @@ static int dispatch_args(const moedisp_shape* s, const void* x, const float* x_s
     a->expert_offsets = const_cast<int32_t*>(expert_offsets);
     a->slot_to_row = slot_to_row;
     a->hdr = (WsHeader*)ws;
-    a->tables_lost = nullptr;
     a->tile_counts = (int32_t*)((char*)ws + w.counts_offset);
     set_pull(a, *s, w, ws, allow_pull && ws_shape == s);
     return MOEDISP_OK;
@@ -551,7 +550,7 @@ int ep_dispatch_notify(const moedisp_shape* s, const int32_t* topk_idx, const in
     const int st = dispatch_args(s, nullptr, nullptr, topk_idx, nullptr, tokens_per_expert, nullptr, nullptr, nullptr,
                                  nullptr, expert_offsets, nullptr, ws, ws_bytes, false, &a);
     if (st) return st;
-    a.tables_lost = &a.hdr->tables_lost;
+    a.pull.split = 1;
     return hip_status(launch_notify_phase(a, true, (hipStream_t)stream));
 }
 
@@ -629,7 +628,7 @@ int ep_dispatch_scatter(const moedisp_shape* s, const void* x, const float* x_sc
     const int st = dispatch_args(s, x, x_scales, topk_idx, topk_weights, tokens_per_expert, recv_x, recv_scales,
                                  recv_src_idx, recv_weights, expert_offsets, slot_to_row, ws, ws_bytes, true, &a);
     if (st) return st;
-    a.tables_lost = &a.hdr->tables_lost;
+    a.pull.split = 1;
     return hip_status(launch_scatter_phase(a, (hipStream_t)stream));
 }
 
@@ -736,7 +735,6 @@ static int quant_args(const moedisp_shape* s, int32_t quant_block, int32_t scale
     a->recv_topk_idx = nullptr;
     a->recv_topk_weights = nullptr;
     a->hdr = (WsHeader*)ws;
-    a->tables_lost = nullptr;
     a->tile_counts = (int32_t*)((char*)ws + w.counts_offset);
     return MOEDISP_OK;
 }
@@ -751,7 +749,7 @@ int ep_dispatch_scatter_quant(const moedisp_shape* s, int32_t quant_block, int32
     const int st = quant_args(s, quant_block, scale_fmt, x, topk_idx, topk_weights, tokens_per_expert, recv_x,
                               recv_scales, recv_src_idx, recv_weights, expert_offsets, slot_to_row, ws, ws_bytes, &a);
     if (st) return st;
-    a.tables_lost = &a.hdr->tables_lost;
+    a.pull.split = 1;
     return hip_status(launch_dispatch_scatter_quant(a, scale_fmt, (hipStream_t)stream));
 }
 

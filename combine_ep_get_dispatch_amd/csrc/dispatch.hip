@@ -182,7 +182,7 @@ __device__ void write_handle(const DispatchArgs& a, const ScatterBlock& b, const
 
 // Whether the balance loss has written where the notify phase left its tables
 // (an entry of such a list can pass every check of its own).
-__device__ inline bool notify_tables_lost(const DispatchArgs& a) { return a.tables_lost && *a.tables_lost; }
+__device__ inline bool notify_tables_lost(const DispatchArgs& a) { return a.pull.split && a.hdr->tables_lost; }
 
 // Workgroup 0: the routed slots must add up to the layout's total.  Whole
 // workgroup (has a barrier); returns this lane's BAD_LAYOUT bit.
@@ -481,9 +481,10 @@ __global__ __launch_bounds__(kMaxDispatchThreads) void moedisp_scatter_pull(Disp
     const int b = xcd + kXcds * m;
     uint32_t err = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) {  // the routed slots must add up to the layout's total
+        const bool lost = notify_tables_lost(a);
         int32_t routed = 0;
         for (int q = 0; q < P.nblk; ++q) routed += a.pull_n[q];
-        if (routed != a.expert_offsets[a.E] || notify_tables_lost(a)) err |= MOEDISP_DEV_BAD_LAYOUT;
+        if ((routed != a.expert_offsets[a.E]) | lost) err |= MOEDISP_DEV_BAD_LAYOUT;
     }
     const int ns = b < P.nblk ? max(0, min(P.tb, a.T - b * P.tb)) * a.k : 0;
     const int i0 = (j - m * P.wpb) * RPW;

@@ -114,7 +114,7 @@ static __device__ inline uint32_t offsets_scan(const DispatchArgs& a, int32_t* s
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.expert_offsets[e] = s[e];
     if (threadIdx.x == 0) {
         a.expert_offsets[a.E] = (int32_t)total;
-        if (a.tables_lost) *a.tables_lost = 0;  // this launch writes them anew
+        if (a.pull.split) a.hdr->tables_lost = 0;  // this launch writes them anew
     }
     return (bad || total > a.capacity) ? (uint32_t)MOEDISP_DEV_BAD_LAYOUT : 0u;
 }

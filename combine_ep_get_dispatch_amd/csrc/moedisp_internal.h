@@ -108,6 +108,9 @@ struct PullPlan {
     int threads;      // copy workgroup lanes
     int units;        // 16-byte units per lane and pass (2, or 3 for rows over 512 units; 4 when compact)
     int wpb;          // copy workgroups per block: ceil(cap_b / rpw)
+    int split;        // not of the plan: a phase of a split dispatch, push or pull (notify clears
+                      // the header's tables_lost, scatter checks it).  It fills a hole: kernel
+                      // arguments 8 bytes longer slowed the copy by 0.4 us (of 90) at T = 4096, H = 7168, k = 8
     long long blocks; // copy grid: kXcds * wpb * ceil(nblk / kXcds), or kXcds * wq when compact
     int compact;      // 1: lists hold the routed entries only; the sort writes masked slots' handles
     int wq;           // compact: copy workgroups per XCD (each takes every wq-th entry of its XCD)
@@ -257,9 +260,6 @@ struct DispatchArgs {
     int32_t* recv_topk_idx;
     float* recv_topk_weights;
     WsHeader* hdr;
-    // the header's word of that name for the two phases of a split dispatch
-    // (notify clears it, scatter checks it), else nullptr
-    uint32_t* tables_lost;
     int32_t* tile_counts;
     // block-pull tables (pull.use != 0)
     PullPlan pull;
