@@ -48,54 +48,48 @@ __device__ inline v4s read_transposed(const char* p) {
 // see into: with the builtin it waits for every load into LDS before a
 // transposing read, and nothing could be loaded ahead (1372 us against 1182
 // for 4096 x 4096 weights and 32768 rows).  There is no result register; the
-// waits are wait_loads_and_sync's and wait_own_loads'.  What stands before
-// the load covers a descriptor that a vector instruction has just written
-// (five wait states).
+// waits are wait_loads_and_sync's and wait_own_loads'.  The s_nop covers
+// the new m0 and a descriptor that a vector instruction has just written (five
+// wait states).
+//
+// The clobber of m0 is what makes the compiler set it anew for a load of its
+// own.  It warns that reserved registers may not be preserved, as none is here.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int SIZE>
 __device__ inline void load_to_lds_unseen(const void* base, const char* lds, int voff) {
     const uint32_t to = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds;
     const v4i rs = {__builtin_amdgcn_readfirstlane((int)(uintptr_t)base),
                     __builtin_amdgcn_readfirstlane((int)((uintptr_t)base >> 32) & 0xFFFF), 0x7FFFFFFF, kRawBufferWord3};
-    int m0;  // put back: m0 is the compiler's, which takes no note of a clobber of it
     if constexpr (SIZE == 16)
-        asm volatile("s_mov_b32 %0, m0\n\ts_nop 2\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-                     "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-                     : "=&s"(m0)
-                     : "s"(to), "v"(voff), "s"(rs)
-                     : "memory");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
+                     "v"(voff), "s"(rs)
+                     : "memory", "m0");
     else if constexpr (SIZE == 4)
-        asm volatile("s_mov_b32 %0, m0\n\ts_nop 2\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-                     "buffer_load_dword %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-                     : "=&s"(m0)
-                     : "s"(to), "v"(voff), "s"(rs)
-                     : "memory");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
+                     "v"(voff), "s"(rs)
+                     : "memory", "m0");
     else
-        asm volatile("s_mov_b32 %0, m0\n\ts_nop 2\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
-                     "buffer_load_ubyte %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
-                     : "=&s"(m0)
-                     : "s"(to), "v"(voff), "s"(rs)
-                     : "memory");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(to),
+                     "v"(voff), "s"(rs)
+                     : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Terms of scale times code: one, but three for fp32 results of FP32 scales.
 constexpr int wgrad_terms(int fmt, bool f32) { return fmt == MOEDISP_SCALE_FP32 && f32 ? 3 : 1; }
 
-// Two values as pairs of bf16: rounded once, or as a sum of three terms of
-// eight bits each, cut off one after the other, so that every step is exact and
-// the terms hold binary32's 24 bits.
+// Two values as pairs of bf16 terms of eight bits each, cut off one after the
+// other, so that every step is exact and three terms hold binary32's 24 bits.
 template <int TERMS>
 __device__ inline void bf16_terms(float v0, float v1, uint32_t o[TERMS]) {
-    if constexpr (TERMS == 1) {
-        o[0] = pack_bf16x2(v0, v1);
-    } else {
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
-            const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
-            o[t] = (b0 >> 16) | (b1 & 0xFFFF0000u);
-            // infinity and NaN are their first term alone
-            v0 = t > 0 || fabsf(v0) < INFINITY ? v0 - __uint_as_float(b0 & 0xFFFF0000u) : 0.0f;
-            v1 = t > 0 || fabsf(v1) < INFINITY ? v1 - __uint_as_float(b1 & 0xFFFF0000u) : 0.0f;
-        }
+    for (int t = 0; t < TERMS; ++t) {
+        const uint32_t b0 = __float_as_uint(v0), b1 = __float_as_uint(v1);
+        o[t] = (b0 >> 16) | (b1 & 0xFFFF0000u);
+        // infinity and NaN are their first term alone
+        v0 = t > 0 || fabsf(v0) < INFINITY ? v0 - __uint_as_float(b0 & 0xFFFF0000u) : 0.0f;
+        v1 = t > 0 || fabsf(v1) < INFINITY ? v1 - __uint_as_float(b1 & 0xFFFF0000u) : 0.0f;
     }
 }
 
@@ -209,30 +203,40 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
         const int xs = *reinterpret_cast<const int*>(raw + u * T::kXRaw + 1024 + lane * 4);
         const float s = FMT == MOEDISP_SCALE_FP32 ? __int_as_float(xs) : ue8m0_value((uint32_t)xs);
         const uint32_t on = step * kStep + x_row < rows ? 0xFFFFFFFFu : 0u;
-        v4u o[TERMS][2];
+        if constexpr (TERMS == 1) {
+            v4u o[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], false);
-            const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], true);
-            uint32_t a[TERMS], b[TERMS];
-            bf16_terms<TERMS>(lo.x * s, lo.y * s, a);
-            bf16_terms<TERMS>(hi.x * s, hi.y * s, b);
+            for (int i = 0; i < 4; ++i) {
+                const v2f lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], false);
+                const v2f hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i], true);
+                o[i >> 1][2 * (i & 1)] = pack_bf16x2(lo.x * s, lo.y * s) & on;
+                o[i >> 1][2 * (i & 1) + 1] = pack_bf16x2(hi.x * s, hi.y * s) & on;
+            }
+            if (kPairs) {
+                const v4u t = {o[0][0], o[0][1], o[1][0], o[1][1]};
+                o[1] = v4u{o[0][2], o[0][3], o[1][2], o[1][3]};
+                o[0] = t;
+            }
+            char* to = x_lds + (step & 1) * T::kXStage;
+            *reinterpret_cast<v4u*>(to + (x_half ? x_at[1] : x_at[0])) = x_half ? o[1] : o[0];
+            *reinterpret_cast<v4u*>(to + (x_half ? x_at[0] : x_at[1])) = x_half ? o[0] : o[1];
+        } else {
+            v4u o[TERMS][2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const v2f v = i & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i >> 1], true)
+                                    : __builtin_amdgcn_cvt_pk_f32_fp8((int)xr[i >> 1], false);
+                uint32_t a[TERMS];
+                bf16_terms<TERMS>(v.x * s, v.y * s, a);
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) o[t][i >> 2][i & 3] = a[t] & on;
+            }
 #pragma unroll
             for (int t = 0; t < TERMS; ++t) {
-                o[t][i >> 1][2 * (i & 1)] = a[t] & on;
-                o[t][i >> 1][2 * (i & 1) + 1] = b[t] & on;
+                char* to = x_lds + ((step & 1) * TERMS + t) * T::kXStage;
+                *reinterpret_cast<v4u*>(to + (x_half ? x_at[1] : x_at[0])) = x_half ? o[t][1] : o[t][0];
+                *reinterpret_cast<v4u*>(to + (x_half ? x_at[0] : x_at[1])) = x_half ? o[t][0] : o[t][1];
             }
-        }
-        if (kPairs) {
-            const v4u t = {o[0][0][0], o[0][0][1], o[0][1][0], o[0][1][1]};
-            o[0][1] = v4u{o[0][0][2], o[0][0][3], o[0][1][2], o[0][1][3]};
-            o[0][0] = t;
-        }
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
-            char* to = x_lds + ((step & 1) * TERMS + t) * T::kXStage;
-            *reinterpret_cast<v4u*>(to + (x_half ? x_at[1] : x_at[0])) = x_half ? o[t][1] : o[t][0];
-            *reinterpret_cast<v4u*>(to + (x_half ? x_at[0] : x_at[1])) = x_half ? o[t][0] : o[t][1];
         }
     };
 
@@ -273,17 +277,21 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad(ExpertWgrad
                 v8bf b[T::kNT], av[2][TERMS];
 #pragma unroll
                 for (int j = 0; j < T::kNT; ++j) b[j] = operand(ds, T::kDyRow, wn / 16 + j);
+                av[0][0] = operand(xst, T::kXRow, wk / 16);
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t) av[0][t] = operand(xst + t * T::kXStage, T::kXRow, wk / 16);
+                for (int t = 1; t < TERMS; ++t) av[0][t] = operand(xst + t * T::kXStage, T::kXRow, wk / 16);
 #pragma unroll
                 for (int i = 0; i < T::kKT; ++i) {
-                    if (i + 1 < T::kKT) {
+                    if (i + 1 < T::kKT) av[(i + 1) & 1][0] = operand(xst, T::kXRow, wk / 16 + i + 1);
 #pragma unroll
-                        for (int t = 0; t < TERMS; ++t)
+                    for (int t = 1; t < TERMS; ++t)
+                        if (i + 1 < T::kKT)
                             av[(i + 1) & 1][t] = operand(xst + t * T::kXStage, T::kXRow, wk / 16 + i + 1);
-                    }
 #pragma unroll
-                    for (int t = TERMS - 1; t >= 0; --t)
+                    for (int j = 0; j < T::kNT; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1][0], b[j], acc[i][j], 0, 0, 0);
+#pragma unroll
+                    for (int t = 1; t < TERMS; ++t)
 #pragma unroll
                         for (int j = 0; j < T::kNT; ++j)
                             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1][t], b[j], acc[i][j], 0, 0, 0);
