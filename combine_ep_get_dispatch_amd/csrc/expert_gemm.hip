@@ -11,11 +11,12 @@
 // in binary32 (UE8M0 scales of bf16 results: inside the instruction).
 //
 // What bounds it.  Few rows: the weights from HBM (decode, 128 tokens top-8 of
-// 256 experts, 7168 -> 4096: 7.4 GB in 1.19 ms, 6.2 TB/s).  128 rows an expert
-// (prefill): the same bytes, 1.63 ms, 4.9 TB/s and 1.2 PFLOP/s.  4096 rows
-// (16384 tokens top-2 of 8, 4096 -> 8192): 1.10 ms, 2.0 PFLOP/s; the products
+// 256 experts, 7168 -> 4096: 7.4 GB in 1.20 ms, 6.2 TB/s).  128 rows an expert
+// (prefill): the same bytes, 1.64 ms, 4.9 TB/s and 1.2 PFLOP/s.  4096 rows
+// (16384 tokens top-2 of 8, 4096 -> 8192): 1.08 ms, 2.0 PFLOP/s; the products
 // alone would take 0.85 ms and the loads alone 0.97 ms: one block's loads, 64
-// KiB per compute unit, take 2 us to arrive and there is LDS for two.
+// KiB per compute unit, take 2 us to arrive (why so long is not known) and there
+// is LDS for two.
 //
 // How.  A workgroup computes a tile of BM rows by BN columns, block of 128
 // channels after block.  Rows and weights go straight into LDS, 128 bytes of 8

@@ -3,16 +3,18 @@
 //
 // Precision.  The scales belong to rows, over which is summed, so they cannot
 // wait until after a matrix instruction: x becomes bf16, scale times code
-// rounded once (by 2^-9 of itself at most; exact for powers of two), and the products are
-// those of the bf16 instruction, added in binary32.  bf16 results, rounded as
-// much themselves, take that.  fp32 results of FP32 scales are to keep
-// binary32's error, over micro-batches too: x becomes a sum of three bf16
+// rounded once (by 2^-8 of itself at most; exact for powers of two), and the
+// products are those of the bf16 instruction, added in binary32.  bf16
+// results, rounded as much themselves, take that.  fp32 results of FP32 scales
+// keep binary32's error, over micro-batches too: x becomes a sum of three bf16
 // terms, exact to binary32, and each has its product.
 //
 // What bounds it.  Many rows (32768 over 8 experts, 4096 x 4096): 1.07 ms, 1.0
-// PFLOP/s; products alone 0.78 ms, loads and LDS alone 0.91 ms.  Few rows (8192
+// PFLOP/s; products alone 0.78 ms, loads and LDS alone 0.91 ms.  Few rows (7782
 // over 64 experts, 7168 x 2048, fp32): the 3.8 GB of results, 0.94 ms, 4.1 TB/s.
-// Three terms: the products, 3.29 and 1.64 ms at these sizes.
+// Three terms: the products, 3.3 and 1.65 ms at these sizes.  An expert's rows
+// are not split, so that a few small experts, or one much longer than the
+// others, leave units without work.
 //
 // How.  A workgroup computes one tile over all rows of its expert, 32 rows a
 // step, three steps of loads under way.  Both operands are contracted over

@@ -436,7 +436,7 @@ int ep_expert_gemm(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale
  *   dw         [E][n][k] bf16 or fp32 (out_dtype).
  * For bf16 results x_scales[r][b] * x[r][k] is rounded to bf16 (exact for UE8M0
  * scales from 2^-116 up); for fp32 results of FP32 scales to binary32, at three
- * times the products (1.7 to 2.7 times the time of large calls).  Products
+ * times the products (1.7 to 3 times the time of large calls).  Products
  * are exact and sums are binary32, in an order that the shape and the row
  * bounds give.  A dy that is not finite makes the sums of its
  * column infinite or NaN.  Sizes, alignment and status bits as for
