@@ -12,6 +12,8 @@ from .binding import (BF16, FP8_E4M3, FP32, SCALE_FP32, SCALE_UE8M0, SCORE_SIGMO
                       ep_get_dispatch_layout, ep_get_dispatch_layout_notify, ep_plan_query, ep_expert_plan_query, ep_balance_plan_query, ep_probe_copy, ep_probe_fill, ep_probe_read,
                       ep_status_string, ep_expert_gemm, ep_expert_wgrad, ep_swiglu_quant, ep_swiglu_backward,
                       ep_balance_workspace_bytes, ep_balance_loss, ep_balance_loss_backward,
+                      ep_expert_gemm_bf16, ep_expert_wgrad_bf16, ep_expert_gemm_w4, ep_swiglu, ep_router_topk,
+                      ep_router_topk_backward, W4_E2M1, W4_INT4, WEIGHTS_KN, WEIGHTS_NK, moedisp_router,
                       ep_workspace_bytes, ep_workspace_init, load, moedisp_balance, moedisp_rows, moedisp_shape)
 
 __all__ = ["BF16", "FP8_E4M3", "FP32", "SCALE_FP32", "SCALE_UE8M0", "SCORE_SIGMOID", "SCORE_SOFTMAX", "EpBuffers", "EpGroupBuffers", "EpPaddedBuffers",
@@ -21,4 +23,6 @@ __all__ = ["BF16", "FP8_E4M3", "FP32", "SCALE_FP32", "SCALE_UE8M0", "SCORE_SIGMO
            "ep_get_dispatch_layout", "ep_get_dispatch_layout_notify", "ep_plan_query", "ep_expert_plan_query", "ep_balance_plan_query", "ep_probe_copy", "ep_probe_fill", "ep_probe_read",
            "ep_status_string", "ep_expert_gemm", "ep_expert_wgrad", "ep_swiglu_quant", "ep_swiglu_backward",
            "ep_balance_workspace_bytes", "ep_balance_loss", "ep_balance_loss_backward",
+           "ep_expert_gemm_bf16", "ep_expert_wgrad_bf16", "ep_expert_gemm_w4", "ep_swiglu", "ep_router_topk",
+           "ep_router_topk_backward", "W4_E2M1", "W4_INT4", "WEIGHTS_KN", "WEIGHTS_NK", "moedisp_router",
            "ep_workspace_bytes", "ep_workspace_init", "load", "moedisp_balance", "moedisp_rows", "moedisp_shape"]

@@ -30,6 +30,14 @@ SCALE_UE8M0 = 1
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 
+# how the weights of ep_expert_gemm_bf16 lie (moedisp_weights_layout)
+WEIGHTS_NK = 0
+WEIGHTS_KN = 1
+
+# weights of 4 bits (moedisp_w4_fmt)
+W4_E2M1 = 0
+W4_INT4 = 1
+
 # host return codes
 OK = 0
 ERR_INVALID_ARG = -1
@@ -52,7 +60,9 @@ EXPORTS = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_dispatch_layout", 
            "ep_layout_dispatch_small", "ep_layout_dispatch_small_padded",
            "ep_combine", "ep_combine_padded", "ep_check_status", "ep_status_string",
            "ep_expert_gemm", "ep_expert_wgrad", "ep_swiglu_quant", "ep_swiglu_backward",
-           "ep_balance_workspace_bytes", "ep_balance_loss", "ep_balance_loss_backward")
+           "ep_balance_workspace_bytes", "ep_balance_loss", "ep_balance_loss_backward",
+           "ep_expert_gemm_bf16", "ep_expert_wgrad_bf16", "ep_expert_gemm_w4", "ep_swiglu", "ep_router_topk",
+           "ep_router_topk_backward")
 # tools (include/moedisp_tools.h): plan query and calibration probes, exported
 # by the same library
 CALIB_EXPORTS = ("ep_plan_query", "ep_expert_plan_query", "ep_balance_plan_query", "ep_probe_read", "ep_probe_copy", "ep_probe_fill")
@@ -104,6 +114,19 @@ class moedisp_balance(C.Structure):
     @classmethod
     def make(cls, num_seqs, seq_len, num_experts, topk, score=SCORE_SOFTMAX, logits_dtype=FP32, coef=1.0):
         return cls(num_seqs, seq_len, num_experts, topk, score, logits_dtype, coef)
+
+
+class moedisp_router(C.Structure):
+    """The router's choice of a batch of tokens (moedisp.h)."""
+    _fields_ = [("num_tokens", C.c_int32), ("num_experts", C.c_int32), ("topk", C.c_int32), ("score", C.c_int32),
+                ("logits_dtype", C.c_int32), ("num_groups", C.c_int32), ("topk_groups", C.c_int32),
+                ("group_best", C.c_int32), ("normalise", C.c_int32), ("scale", C.c_float)]
+
+    @classmethod
+    def make(cls, num_tokens, num_experts, topk, score=SCORE_SOFTMAX, logits_dtype=FP32, groups=1, topk_groups=1,
+             group_best=2, normalise=True, scale=1.0):
+        return cls(num_tokens, num_experts, topk, score, logits_dtype, groups, topk_groups, group_best,
+                   1 if normalise else 0, scale)
 
 
 class moedisp_expert_plan_info(C.Structure):
@@ -230,6 +253,19 @@ def load(path: str = LIB_PATH):
     L.ep_balance_loss.restype = C.c_int
     L.ep_balance_loss_backward.argtypes = [Bl, P, P, P, P, P, P, P]
     L.ep_balance_loss_backward.restype = C.c_int
+    Rt = C.POINTER(moedisp_router)
+    L.ep_expert_gemm_bf16.argtypes = [R, i32, i32, i32, P, P, P, P, i32, P, sz, P]
+    L.ep_expert_gemm_bf16.restype = C.c_int
+    L.ep_expert_wgrad_bf16.argtypes = [R, i32, i32, P, P, P, P, i32, i32, P, sz, P]
+    L.ep_expert_wgrad_bf16.restype = C.c_int
+    L.ep_expert_gemm_w4.argtypes = [R, i32, i32, i32, P, P, P, P, P, i32, P, sz, P]
+    L.ep_expert_gemm_w4.restype = C.c_int
+    L.ep_swiglu.argtypes = [R, i32, P, P, P, P, sz, P]
+    L.ep_swiglu.restype = C.c_int
+    L.ep_router_topk.argtypes = [Rt, P, P, P, P, P, P]
+    L.ep_router_topk.restype = C.c_int
+    L.ep_router_topk_backward.argtypes = [Rt, P, P, P, P, P, sz, P]
+    L.ep_router_topk_backward.restype = C.c_int
     L.ep_plan_query.argtypes = [S, C.POINTER(moedisp_plan_info), C.c_size_t]
     L.ep_plan_query.restype = C.c_int
     L.ep_expert_plan_query.argtypes = [R, i32, i32, i32, i32, C.POINTER(moedisp_expert_plan_info), sz]
@@ -267,6 +303,7 @@ _U16 = tuple(d for d in (getattr(torch, "uint16", None),) if d is not None)
 _I32 = (torch.int32,) + tuple(d for d in (getattr(torch, "uint32", None),) if d is not None)
 _ROWS_BF16 = (torch.bfloat16, torch.int16, torch.uint8) + _U16
 _ROWS_FP8 = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+_ROWS_W4 = (torch.uint8, torch.int8) + tuple(d for d in (getattr(torch, "float4_e2m1fn_x2", None),) if d is not None)
 _F32 = (torch.float32,)
 _INT32 = (torch.int32,)
 _BYTES = None  # any element type (workspaces, probe buffers)
@@ -780,6 +817,81 @@ def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, d
     at = A.arg("ws", ws, _BYTES, 1)
     dev, st = A.on_device(stream)
     _on(dev, A.call, C.byref(rows), inner, scale_fmt, *args, at, ws.nbytes, st)
+
+
+def ep_swiglu(rows, inner, gu, row_bounds, h, ws, stream=None):
+    A = _Args("ep_swiglu")
+    inner = int(inner)
+    R, _, bounds = _rows_of(A, rows, row_bounds)
+    I = max(inner, 0)
+    args = (A.arg("gu", gu, _ROWS_BF16, R * I * 4), bounds, A.arg("h", h, _ROWS_BF16, R * I * 2, written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), inner, *args, at, ws.nbytes, st)
+
+
+def ep_expert_gemm_bf16(rows, n, k, w_layout, x, w, row_bounds, y, out_dtype, ws, stream=None):
+    A = _Args("ep_expert_gemm_bf16")
+    n, k, w_layout, out_dtype = int(n), int(k), int(w_layout), int(out_dtype)
+    R, E, bounds = _rows_of(A, rows, row_bounds)
+    N, K = max(n, 0), max(k, 0)
+    args = (A.arg("x", x, _ROWS_BF16, R * K * 2), A.arg("w", w, _ROWS_BF16, E * N * K * 2), bounds,
+            A.arg("y", y, _out_dtypes(out_dtype), R * N * (4 if out_dtype == FP32 else 2), written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), n, k, w_layout, *args, out_dtype, at, ws.nbytes, st)
+
+
+def ep_expert_wgrad_bf16(rows, n, k, x, dy, row_bounds, dw, out_dtype, accumulate, ws, stream=None):
+    A = _Args("ep_expert_wgrad_bf16")
+    n, k, out_dtype = int(n), int(k), int(out_dtype)
+    R, E, bounds = _rows_of(A, rows, row_bounds)
+    N, K = max(n, 0), max(k, 0)
+    args = (A.arg("x", x, _ROWS_BF16, R * K * 2), A.arg("dy", dy, _ROWS_BF16, R * N * 2), bounds,
+            A.arg("dw", dw, _out_dtypes(out_dtype), E * N * K * (4 if out_dtype == FP32 else 2), written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), n, k, *args, out_dtype, 1 if accumulate else 0, at, ws.nbytes, st)
+
+
+def ep_expert_gemm_w4(rows, n, k, w4_fmt, x, w, w_scales, row_bounds, y, out_dtype, ws, stream=None):
+    A = _Args("ep_expert_gemm_w4")
+    n, k, w4_fmt, out_dtype = int(n), int(k), int(w4_fmt), int(out_dtype)
+    R, E, bounds = _rows_of(A, rows, row_bounds)
+    N, K = max(n, 0), max(k, 0)
+    sdt, sbytes = (_ROWS_BF16, E * (K // 128) * N * 2) if w4_fmt == W4_INT4 else (_U8, E * (K // 32) * N)
+    args = (A.arg("x", x, _ROWS_BF16, R * K * 2), A.arg("w", w, _ROWS_W4, E * N * (K // 2)),
+            A.arg("w_scales", w_scales, sdt, sbytes), bounds,
+            A.arg("y", y, _out_dtypes(out_dtype), R * N * (4 if out_dtype == FP32 else 2), written=True))
+    at = A.arg("ws", ws, _BYTES, 1)
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(rows), n, k, w4_fmt, *args, out_dtype, at, ws.nbytes, st)
+
+
+def _choice(A, r, logits):
+    """T, E, k, the logits' types and bytes, and their address."""
+    T, E, k = max(r.num_tokens, 0), max(r.num_experts, 0), max(r.topk, 0)
+    dt, nbytes = (_BF16, T * E * 2) if r.logits_dtype == BF16 else (_F32, T * E * 4)
+    return T, E, k, dt, nbytes, A.arg("logits", logits, dt, nbytes)
+
+
+def ep_router_topk(router, logits, bias, live, topk_idx, topk_weights, stream=None):
+    A = _Args("ep_router_topk")
+    T, E, k, _, _, z = _choice(A, router, logits)
+    args = (z, A.arg("bias", bias, _F32, 4 * E, optional=True), A.arg("live", live, _U8, T, optional=True),
+            A.arg("topk_idx", topk_idx, _INT32, 4 * T * k, written=True),
+            A.arg("topk_weights", topk_weights, _F32, 4 * T * k, written=True))
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(router), *args, st)
+
+
+def ep_router_topk_backward(router, logits, topk_idx, d_topk_weights, d_logits, ws, stream=None):
+    A = _Args("ep_router_topk_backward")
+    T, E, k, dt, nbytes, z = _choice(A, router, logits)
+    args = (z, A.arg("topk_idx", topk_idx, _INT32, 4 * T * k), A.arg("d_topk_weights", d_topk_weights, _F32, 4 * T * k),
+            A.arg("d_logits", d_logits, dt, nbytes, written=True), A.arg("ws", ws, _BYTES, 1))
+    dev, st = A.on_device(stream)
+    _on(dev, A.call, C.byref(router), *args, ws.nbytes, st)
 
 
 def ep_balance_workspace_bytes(balance) -> int:

@@ -10,7 +10,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoedisp.so")
 SOURCES = ["capi.hip", "layout.hip", "notify.hip", "dispatch.hip", "decode.hip", "combine.hip", "util.hip",
-           "capi_experts.hip", "expert_gemm.hip", "expert_wgrad.hip", "swiglu.hip", "balance.hip"]
+           "capi_experts.hip", "expert_gemm.hip", "expert_wgrad.hip", "expert_gemm_bf16.hip",
+           "expert_wgrad_bf16.hip", "expert_gemm_w4.hip", "swiglu.hip", "balance.hip", "router.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

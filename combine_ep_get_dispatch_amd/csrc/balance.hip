@@ -22,39 +22,6 @@ constexpr int kBalThreads = 256;
 constexpr int kSeqThreads = 1024;
 constexpr int kSeqCols = 64;  // experts of a workgroup that sums tiles
 
-template <int CTRL>
-__device__ inline float dpp(float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
-}
-
-// op over a row's LPR lanes (aligned), every lane gets it: exchanges by
-// register moves, no LDS.  After steps 1 and 2 the lanes of 4 agree, so
-// mirroring 8 and then 16 lanes meets the other half.
-template <int LPR, class OP>
-__device__ inline float row_reduce(float v, OP op) {
-    if (LPR > 1) v = op(v, dpp<0xB1>(v));
-    if (LPR > 2) v = op(v, dpp<0x4E>(v));
-    if (LPR > 4) v = op(v, dpp<0x141>(v));
-    if (LPR > 8) v = op(v, dpp<0x140>(v));
-    if (LPR > 16) {  // both 16-lane rows' values, in the same order for both
-        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
-    }
-    if (LPR > 32) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-        v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
-    }
-    return v;
-}
-template <int LPR>
-__device__ inline float lanes_sum(float v) {
-    return row_reduce<LPR>(v, [](float x, float y) { return x + y; });
-}
-template <int LPR>
-__device__ inline float lanes_max(float v) {
-    return row_reduce<LPR>(v, [](float x, float y) { return fmaxf(x, y); });
-}
-
 template <int LPR>
 __device__ inline int lanes_sum(int v) {
     return __float_as_int(row_reduce<LPR>(__int_as_float(v), [](float x, float y) {

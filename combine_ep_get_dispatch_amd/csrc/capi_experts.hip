@@ -81,6 +81,42 @@ int check_inner(int inner, int scale_fmt) {
     return check_scale_fmt(scale_fmt);
 }
 
+// Columns and channels of the products of bf16 rows, multiples of n_step and k_step.
+int check_bf16_product(int n, int k, int n_step, int k_step, int out_dtype) {
+    if (n <= 0 || k <= 0) return MOEDISP_ERR_INVALID_ARG;
+    if (n % n_step != 0 || k % k_step != 0 || n > kMaxColumns || k > kMaxChannels) return MOEDISP_ERR_UNSUPPORTED;
+    return out_dtype == MOEDISP_BF16 || out_dtype == MOEDISP_FP32 ? MOEDISP_OK : MOEDISP_ERR_UNSUPPORTED;
+}
+
+int check_router(const moedisp_router* r) {
+    if (!r) return MOEDISP_ERR_INVALID_ARG;
+    if (r->num_tokens < 0 || r->num_experts < 1 || r->topk < 1 || r->topk > r->num_experts || r->num_groups < 1 ||
+        r->num_experts % r->num_groups != 0 || r->topk_groups < 1 || r->topk_groups > r->num_groups)
+        return MOEDISP_ERR_INVALID_ARG;
+    if ((r->group_best != 1 && r->group_best != 2) || (r->normalise != 0 && r->normalise != 1) || !isfinite(r->scale))
+        return MOEDISP_ERR_INVALID_ARG;
+    if (r->num_experts > kMaxExperts || r->topk > kMaxTopk || r->num_groups > 64) return MOEDISP_ERR_UNSUPPORTED;
+    if (r->score != MOEDISP_SCORE_SOFTMAX && r->score != MOEDISP_SCORE_SIGMOID) return MOEDISP_ERR_UNSUPPORTED;
+    if (r->logits_dtype != MOEDISP_BF16 && r->logits_dtype != MOEDISP_FP32) return MOEDISP_ERR_UNSUPPORTED;
+    if (r->num_tokens >= (1ll << 30) / r->topk) return MOEDISP_ERR_UNSUPPORTED;
+    return MOEDISP_OK;
+}
+
+RouterArgs router_args(const moedisp_router& r) {
+    RouterArgs a = {};
+    a.T = r.num_tokens;
+    a.E = r.num_experts;
+    a.k = r.topk;
+    a.groups = r.num_groups;
+    a.topk_groups = r.topk_groups;
+    a.per_group = r.num_experts / r.num_groups;
+    a.group_best = r.group_best;
+    a.sigmoid = r.score == MOEDISP_SCORE_SIGMOID;
+    a.normalise = r.normalise != 0;
+    a.scale = r.scale;
+    return a;
+}
+
 int check_balance(const moedisp_balance* b) {
     if (!b) return MOEDISP_ERR_INVALID_ARG;
     if (b->num_seqs < 0 || b->seq_len < 0 || b->num_experts < 1 || b->topk < 1 || b->topk > b->num_experts)
@@ -235,6 +271,122 @@ int ep_swiglu_backward(const moedisp_rows* rows, int32_t inner, int32_t scale_fm
     a.q_scales = dgu_scales;
     a.hdr = (WsHeader*)ws;
     return status_of(launch_swiglu_backward(a, scale_fmt, (hipStream_t)stream));
+}
+
+int ep_swiglu(const moedisp_rows* rows, int32_t inner, const void* gu, const int32_t* row_bounds, void* h, void* ws,
+              size_t ws_bytes, void* stream) {
+    int st = check_rows(rows, row_bounds);
+    if (st || (st = check_inner(inner, MOEDISP_SCALE_FP32))) return st;
+    if (rows->max_rows > 0 && (!gu || !h)) return MOEDISP_ERR_INVALID_ARG;
+    if (!aligned_to(gu, 16) || !aligned_to(h, 16)) return MOEDISP_ERR_MISALIGNED;
+    if ((st = check_header(ws, ws_bytes))) return st;
+    SwigluArgs a = {};
+    a.r = rows_arg(*rows, row_bounds);
+    a.inner = inner;
+    a.blocks = inner / kScaleBlock;
+    a.gu = (const uint16_t*)gu;
+    a.h = (uint16_t*)h;
+    a.hdr = (WsHeader*)ws;
+    return status_of(launch_swiglu_bf16(a, (hipStream_t)stream));
+}
+
+int ep_expert_gemm_bf16(const moedisp_rows* rows, int32_t n, int32_t k, int32_t w_layout, const void* x, const void* w,
+                        const int32_t* row_bounds, void* y, int32_t out_dtype, void* ws, size_t ws_bytes,
+                        void* stream) {
+    int st = check_rows(rows, row_bounds);
+    if (st || (st = check_bf16_product(n, k, 8, 8, out_dtype))) return st;
+    if (w_layout != MOEDISP_WEIGHTS_NK && w_layout != MOEDISP_WEIGHTS_KN) return MOEDISP_ERR_UNSUPPORTED;
+    if (!w || (rows->max_rows > 0 && (!x || !y))) return MOEDISP_ERR_INVALID_ARG;
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(y, 16)) return MOEDISP_ERR_MISALIGNED;
+    if ((st = check_header(ws, ws_bytes))) return st;
+    ExpertBf16Args a = {};
+    a.r = rows_arg(*rows, row_bounds);
+    a.n = n;
+    a.k = k;
+    a.x = (const uint16_t*)x;
+    a.w = (const uint16_t*)w;
+    a.y = y;
+    a.hdr = (WsHeader*)ws;
+    return status_of(launch_expert_gemm_bf16(a, mean_rows(*rows), w_layout == MOEDISP_WEIGHTS_KN,
+                                             out_dtype == MOEDISP_FP32, (hipStream_t)stream));
+}
+
+int ep_expert_wgrad_bf16(const moedisp_rows* rows, int32_t n, int32_t k, const void* x, const void* dy,
+                         const int32_t* row_bounds, void* dw, int32_t out_dtype, int32_t accumulate, void* ws,
+                         size_t ws_bytes, void* stream) {
+    int st = check_rows(rows, row_bounds);
+    if (st || (st = check_bf16_product(n, k, 8, 8, out_dtype))) return st;
+    if (accumulate != 0 && accumulate != 1) return MOEDISP_ERR_INVALID_ARG;
+    if (accumulate && out_dtype != MOEDISP_FP32) return MOEDISP_ERR_UNSUPPORTED;
+    if (!dw || (rows->max_rows > 0 && (!x || !dy))) return MOEDISP_ERR_INVALID_ARG;
+    if (!aligned_to(x, 16) || !aligned_to(dy, 16) || !aligned_to(dw, 16)) return MOEDISP_ERR_MISALIGNED;
+    if ((st = check_header(ws, ws_bytes))) return st;
+    ExpertBf16Args a = {};
+    a.r = rows_arg(*rows, row_bounds);
+    a.n = n;
+    a.k = k;
+    a.x = (const uint16_t*)x;
+    a.dy = (const uint16_t*)dy;
+    a.y = dw;
+    a.hdr = (WsHeader*)ws;
+    return status_of(launch_expert_wgrad_bf16(a, out_dtype == MOEDISP_FP32, accumulate != 0, (hipStream_t)stream));
+}
+
+int ep_expert_gemm_w4(const moedisp_rows* rows, int32_t n, int32_t k, int32_t w4_fmt, const void* x, const void* w,
+                      const void* w_scales, const int32_t* row_bounds, void* y, int32_t out_dtype, void* ws,
+                      size_t ws_bytes, void* stream) {
+    int st = check_rows(rows, row_bounds);
+    if (st || (st = check_bf16_product(n, k, 16, 128, out_dtype))) return st;
+    if (w4_fmt != MOEDISP_W4_E2M1 && w4_fmt != MOEDISP_W4_INT4) return MOEDISP_ERR_UNSUPPORTED;
+    if (!w || !w_scales || (rows->max_rows > 0 && (!x || !y))) return MOEDISP_ERR_INVALID_ARG;
+    if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(y, 16) || !aligned_to(w_scales, 4))
+        return MOEDISP_ERR_MISALIGNED;
+    if ((st = check_header(ws, ws_bytes))) return st;
+    ExpertW4Args a = {};
+    a.r = rows_arg(*rows, row_bounds);
+    a.n = n;
+    a.k = k;
+    a.x = (const uint16_t*)x;
+    a.w = (const uint8_t*)w;
+    a.w_scales = w_scales;
+    a.y = y;
+    a.hdr = (WsHeader*)ws;
+    return status_of(
+        launch_expert_gemm_w4(a, mean_rows(*rows), w4_fmt, out_dtype == MOEDISP_FP32, (hipStream_t)stream));
+}
+
+int ep_router_topk(const moedisp_router* r, const void* logits, const float* bias, const uint8_t* live,
+                   int32_t* topk_idx, float* topk_weights, void* stream) {
+    const int st = check_router(r);
+    if (st) return st;
+    if (r->num_tokens > 0 && (!logits || !topk_idx || !topk_weights)) return MOEDISP_ERR_INVALID_ARG;
+    if (!aligned_to(logits, 16) || !aligned_to(bias, 4) || !aligned_to(topk_idx, 4) || !aligned_to(topk_weights, 4))
+        return MOEDISP_ERR_MISALIGNED;
+    RouterArgs a = router_args(*r);
+    a.logits = logits;
+    a.bias = bias;
+    a.live = live;
+    a.topk_idx = topk_idx;
+    a.weights = topk_weights;
+    return status_of(launch_router(a, r->logits_dtype == MOEDISP_BF16, (hipStream_t)stream));
+}
+
+int ep_router_topk_backward(const moedisp_router* r, const void* logits, const int32_t* topk_idx,
+                            const float* d_topk_weights, void* d_logits, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_router(r);
+    if (st) return st;
+    if (r->num_tokens > 0 && (!logits || !topk_idx || !d_topk_weights || !d_logits)) return MOEDISP_ERR_INVALID_ARG;
+    if (!aligned_to(logits, 16) || !aligned_to(topk_idx, 4) || !aligned_to(d_topk_weights, 4) ||
+        !aligned_to(d_logits, 16))
+        return MOEDISP_ERR_MISALIGNED;
+    if ((st = check_header(ws, ws_bytes))) return st;
+    RouterArgs a = router_args(*r);
+    a.logits = logits;
+    a.topk_idx = const_cast<int32_t*>(topk_idx);
+    a.weights = const_cast<float*>(d_topk_weights);
+    a.d_logits = d_logits;
+    a.hdr = (WsHeader*)ws;
+    return status_of(launch_router_backward(a, r->logits_dtype == MOEDISP_BF16, (hipStream_t)stream));
 }
 
 size_t ep_balance_workspace_bytes(const moedisp_balance* b) {

@@ -46,7 +46,6 @@ __device__ inline v8i read_frag(const char* row, int sw, int q) {
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
 // 8 E4M3 codes (dwords 2j, 2j+1 of a fragment) as bf16, exactly.
@@ -63,12 +62,6 @@ template <int FMT>
 __device__ inline float scale_value(int bits) {
     return FMT == MOEDISP_SCALE_FP32 ? __int_as_float(bits) : ue8m0_value((uint32_t)bits);
 }
-
-// LDS reads of 16 bytes go in groups of 16 lanes ({0-3, 12-15, 20-27} and its
-// like) over 64 banks.  Rows of an operand read: 0-3, 8-11, 16-19, 24-27 for
-// the weights of bf16 results (see the columns' order), else 0-15.
-__device__ inline int swizzle_w(int row) { return ((row >> 1) & 1) | (((row >> 3) & 3) << 1); }
-__device__ inline int swizzle_x(int row) { return (row >> 1) & 7; }
 
 template <int BM, int BN, int WM, int WN, int WS, int XS, int FMT, bool F32>
 struct Tile {

@@ -27,56 +27,8 @@
 namespace moedisp {
 namespace {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef short v4s __attribute__((ext_vector_type(4)));
-
 constexpr int kStep = 32;    // rows per step: the contraction of one matrix instruction
 constexpr int kStages = 4;   // steps under way or in use
-
-// In LDS both operands lie by rows, in bf16, as units of 32 bytes (16 columns
-// or channels); unit u of row r is stored at u ^ unit_swizzle(r).  An operand
-// read takes the same unit of 4 rows for each of 4 groups of 16 lanes (rows r,
-// r + 8, r + 16, r + 24): the swizzle puts 8 of these 16 on different banks,
-// as many as 64 banks hold.
-__device__ inline int unit_swizzle(int r) { return (r & 3) | ((r >> 1) & 4); }
-
-// Lane 4m + i of 16 reads 8 bytes of row m of four; lane c gets column c of
-// the 16 that the four rows' pieces make up, a row each.
-__device__ inline v4s read_transposed(const char* p) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)p);
-}
-
-// load_to_lds (experts_common.h) by an instruction that the compiler does not
-// see into: with the builtin it waits for every load into LDS before a
-// transposing read, and nothing could be loaded ahead (1372 us against 1182
-// for 4096 x 4096 weights and 32768 rows).  There is no result register; the
-// waits are wait_loads_and_sync's and wait_own_loads'.  The s_nop covers
-// the new m0 and a descriptor that a vector instruction has just written (five
-// wait states).
-//
-// The clobber of m0 is what makes the compiler set it anew for a load of its
-// own.  It warns that reserved registers may not be preserved, as none is here.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <int SIZE>
-__device__ inline void load_to_lds_unseen(const void* base, const char* lds, int voff) {
-    const uint32_t to = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)lds;
-    const v4i rs = {__builtin_amdgcn_readfirstlane((int)(uintptr_t)base),
-                    __builtin_amdgcn_readfirstlane((int)((uintptr_t)base >> 32) & 0xFFFF), 0x7FFFFFFF, kRawBufferWord3};
-    if constexpr (SIZE == 16)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to),
-                     "v"(voff), "s"(rs)
-                     : "memory", "m0");
-    else if constexpr (SIZE == 4)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(to),
-                     "v"(voff), "s"(rs)
-                     : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_ubyte %1, %2, 0 offen lds" ::"s"(to),
-                     "v"(voff), "s"(rs)
-                     : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 // Terms of scale times code: one, but three for fp32 results of FP32 scales.
 constexpr int wgrad_terms(int fmt, bool f32) { return fmt == MOEDISP_SCALE_FP32 && f32 ? 3 : 1; }
@@ -93,12 +45,6 @@ __device__ inline void bf16_terms(float v0, float v1, uint32_t o[TERMS]) {
         v0 = t > 0 || fabsf(v0) < INFINITY ? v0 - __uint_as_float(b0 & 0xFFFF0000u) : 0.0f;
         v1 = t > 0 || fabsf(v1) < INFINITY ? v1 - __uint_as_float(b1 & 0xFFFF0000u) : 0.0f;
     }
-}
-
-// At most N of the wave's own loads are under way.
-template <int N>
-__device__ inline void wait_own_loads() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 // Tile of TN columns of dy by TK channels of x; WN x WK waves; x as a sum of

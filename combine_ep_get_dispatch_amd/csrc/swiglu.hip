@@ -1,5 +1,5 @@
-// Gated activation between an expert's two products, with quantisation, and
-// its gradient:
+// Gated activation between an expert's two products, with quantisation or in
+// bf16, and its gradient:
 //     h = g * s * u,  s = 1 / (1 + exp(-g))
 //     dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s
 // each binary32, and E4M3 codes with one scale per block of 128 channels.
@@ -67,6 +67,10 @@ __device__ inline void unpack8(v4u v, float f[8]) {
     }
 }
 
+__device__ inline v4u pack8(const float f[8]) {
+    return v4u{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+}
+
 // Codes and scale of a block from its 16 lanes' 8 values each.
 template <int FMT>
 __device__ inline void quantise(const float f[8], uint8_t* q, void* scales, size_t at, bool lead) {
@@ -113,6 +117,8 @@ __device__ inline void quantise(const float f[8], uint8_t* q, void* scales, size
     }
 }
 
+constexpr int kBf16 = -1;  // FMT of the forward pass in bf16
+
 template <int FMT, bool BACKWARD>
 __global__ __launch_bounds__(kSwigluThreads, BACKWARD ? 7 : 8) void moedisp_swiglu(SwigluArgs a) {
     int first, end;
@@ -144,7 +150,10 @@ __global__ __launch_bounds__(kSwigluThreads, BACKWARD ? 7 : 8) void moedisp_swig
             if (!BACKWARD) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
-                quantise<FMT>(o, a.q + (size_t)row * a.inner + c, a.q_scales, (size_t)row * a.blocks + b, l == 0);
+                if constexpr (FMT == kBf16)
+                    *reinterpret_cast<v4u*>(a.h + (size_t)row * a.inner + c) = pack8(o);
+                else
+                    quantise<FMT>(o, a.q + (size_t)row * a.inner + c, a.q_scales, (size_t)row * a.blocks + b, l == 0);
             } else {
                 float d[8], o2[8];
                 unpack8(dv, d);
@@ -155,12 +164,8 @@ __global__ __launch_bounds__(kSwigluThreads, BACKWARD ? 7 : 8) void moedisp_swig
                     o2[i] = d[i] * (g[i] * s);
                 }
                 if (a.dgu) {
-                    const v4u v = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                   pack_bf16x2(o[6], o[7])};
-                    const v4u v2 = {pack_bf16x2(o2[0], o2[1]), pack_bf16x2(o2[2], o2[3]), pack_bf16x2(o2[4], o2[5]),
-                                    pack_bf16x2(o2[6], o2[7])};
-                    *reinterpret_cast<v4u*>(a.dgu + (size_t)row * 2 * a.inner + c) = v;
-                    *reinterpret_cast<v4u*>(a.dgu + (size_t)row * 2 * a.inner + a.inner + c) = v2;
+                    *reinterpret_cast<v4u*>(a.dgu + (size_t)row * 2 * a.inner + c) = pack8(o);
+                    *reinterpret_cast<v4u*>(a.dgu + (size_t)row * 2 * a.inner + a.inner + c) = pack8(o2);
                 }
                 if (a.q) {
                     quantise<FMT>(o, a.q + (size_t)row * 2 * a.inner + c, a.q_scales, (size_t)row * 2 * a.blocks + b,
@@ -198,6 +203,11 @@ long long swiglu_blocks(int max_rows, int blocks, bool backward) {
 
 hipError_t launch_swiglu(const SwigluArgs& a, int scale_fmt, hipStream_t stream) {
     return launch<false>(a, scale_fmt, stream);
+}
+hipError_t launch_swiglu_bf16(const SwigluArgs& a, hipStream_t stream) {
+    const long long blocks = swiglu_blocks(a.r.max_rows, a.blocks, false);
+    hipLaunchKernelGGL((moedisp_swiglu<kBf16, false>), dim3((unsigned)blocks), dim3(kSwigluThreads), 0, stream, a);
+    return hipGetLastError();
 }
 hipError_t launch_swiglu_backward(const SwigluArgs& a, int scale_fmt, hipStream_t stream) {
     return launch<true>(a, scale_fmt, stream);

@@ -471,11 +471,120 @@ int ep_swiglu_backward(const moedisp_rows* rows, int32_t inner, int32_t scale_fm
                        const int32_t* row_bounds, void* dgu, void* dgu_q, void* dgu_scales, void* ws,
                        size_t ws_bytes, void* stream);
 
-/* Scores of the router whose balance is measured. */
+/* ep_swiglu_quant without the quantisation: h bf16 [max_rows][inner], rounded
+ * once.  An infinite g gives an infinite product or NaN, as the formula does
+ * (an infinite negative g times 0 is NaN). */
+int ep_swiglu(const moedisp_rows* rows, int32_t inner, const void* gu, const int32_t* row_bounds, void* h, void* ws,
+              size_t ws_bytes, void* stream);
+
+/* How the weights of ep_expert_gemm_bf16 lie. */
+typedef enum {
+    MOEDISP_WEIGHTS_NK = 0,  /* w[e][n][k] */
+    MOEDISP_WEIGHTS_KN = 1   /* w[e][k][n] */
+} moedisp_weights_layout;
+
+/* Product of every expert's bf16 rows with its bf16 weights:
+ *   y[r][n] = sum over k of x[r][k] * w[e][n][k] (or w[e][k][n]),  e = r's expert,
+ * products exact, accumulated in binary32, rounded once to out_dtype.
+ *   n          columns of y, n % 8 == 0, in [8, 2^20].
+ *   k          channels of x, k % 8 == 0, in [8, 65536].
+ *   x          bf16 [max_rows][k];  w bf16 [E][n][k] or [E][k][n] (w_layout).
+ *   y          [max_rows][n] bf16 or fp32 (out_dtype).
+ * The gradient of x is the same call with y's gradient as x, n and k
+ * exchanged, the other w_layout and the same weights.  Rows, bounds, ws,
+ * overlap and alignment as said at moedisp_rows.  The order of the sums
+ * depends on the shape only, so equal inputs give equal bits.  Status bits:
+ * BAD_LAYOUT. */
+int ep_expert_gemm_bf16(const moedisp_rows* rows, int32_t n, int32_t k, int32_t w_layout, const void* x, const void* w,
+                        const int32_t* row_bounds, void* y, int32_t out_dtype, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Gradient of the weights [E][n][k] of ep_expert_gemm_bf16:
+ *   dw[e][n][k] = sum over e's rows r of dy[r][n] * x[r][k],
+ * plus the previous dw[e][n][k] if accumulate is 1 (fp32 only; 0: dw is
+ * overwritten, with zeros for an expert without rows).  For weights [E][k][n]
+ * exchange dy with x, and n with k.
+ *   x bf16 [max_rows][k];  dy bf16 [max_rows][n];  dw [E][n][k] bf16 or fp32.
+ * Products are exact and sums are binary32, in an order that the shape and the
+ * row bounds give.  Sizes, alignment and status bits as for
+ * ep_expert_gemm_bf16. */
+int ep_expert_wgrad_bf16(const moedisp_rows* rows, int32_t n, int32_t k, const void* x, const void* dy,
+                         const int32_t* row_bounds, void* dw, int32_t out_dtype, int32_t accumulate, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* Weights of 4 bits. */
+typedef enum {
+    MOEDISP_W4_E2M1 = 0,  /* OCP E2M1 codes (sign, 0 0.5 1 1.5 2 3 4 6), a UE8M0 scale per 32 channels */
+    MOEDISP_W4_INT4 = 1   /* code - 8, that is -8 .. 7, a bf16 scale per 128 channels */
+} moedisp_w4_fmt;
+
+/* Product of every expert's bf16 rows with its 4-bit weights:
+ *   y[r][n] = sum over k of x[r][k] * w_scales[e][k/g][n] * c[e][n][k],
+ * g = 32 or 128 (w4_fmt), accumulated in binary32, rounded once to out_dtype.
+ *   n          columns of y, n % 16 == 0, in [16, 2^20].
+ *   k          channels of x, k % 128 == 0, in [128, 65536].
+ *   x          bf16 [max_rows][k].
+ *   w          codes [E][n][k/2]: a byte holds channel 2i in its low half and
+ *              2i + 1 in its high half.
+ *   w_scales   [E][k/g][n], uint8 (2^(byte - 127), 255 is NaN) or bf16: the
+ *              scales of one group of channels lie together.
+ *   y          [max_rows][n] bf16 or fp32 (out_dtype).
+ * E2M1: a weight times its scale is taken as bf16 number, infinite beyond its
+ * range.  INT4: sums over a group's x times code + 8 are binary32 and at most
+ * 5 times as large as those of x times 8, so x has to stay below 2^122; a row
+ * that holds an infinity gives NaN.  Rows, bounds, ws, overlap and alignment
+ * as said at moedisp_rows (UE8M0 scales: 4 bytes, bf16 scales: 4 bytes).
+ * Equal inputs give equal bits.  Status bits: BAD_LAYOUT. */
+int ep_expert_gemm_w4(const moedisp_rows* rows, int32_t n, int32_t k, int32_t w4_fmt, const void* x, const void* w,
+                      const void* w_scales, const int32_t* row_bounds, void* y, int32_t out_dtype, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* Scores of the router: of its choice, and where its balance is measured. */
 typedef enum {
     MOEDISP_SCORE_SOFTMAX = 0,  /* p_e = exp(z_e) / sum_j exp(z_j) */
-    MOEDISP_SCORE_SIGMOID = 1   /* p_e = s(z_e) / sum_j s(z_j), s(v) = 1 / (1 + exp(-v)) */
+    MOEDISP_SCORE_SIGMOID = 1   /* p_e = s(z_e) / sum_j s(z_j), s(v) = 1 / (1 + exp(-v)); the choice's score is s(z_e) */
 } moedisp_score;
+
+/* The router's choice of a batch of tokens. */
+typedef struct {
+    int32_t num_tokens;    /* T >= 0, T < 2^30 / topk */
+    int32_t num_experts;   /* E in [1, 4096] */
+    int32_t topk;          /* k in [1, 32], k <= E */
+    int32_t score;         /* moedisp_score */
+    int32_t logits_dtype;  /* MOEDISP_BF16 or MOEDISP_FP32 */
+    int32_t num_groups;    /* in [1, 64], E % num_groups == 0: experts e / (E / num_groups) */
+    int32_t topk_groups;   /* groups that may be chosen from, in [1, num_groups] */
+    int32_t group_best;    /* 1 or 2: a group's value is the sum of its so many largest choice values */
+    int32_t normalise;     /* 1: a token's weights sum to scale; 0: weights are scale * score */
+    float scale;           /* finite */
+} moedisp_router;
+
+/* The choice of k experts for each token, and their weights: what dispatch,
+ * combine and the balance loss take as topk_idx and topk_weights.
+ *   choice value  the logit where there is neither bias nor groups, else
+ *                 score + bias, to 2^-40 of its value.
+ *   num_groups    above 1: only the topk_groups groups of the largest value
+ *                 are chosen from.
+ * Among equals the lowest index comes first.  The k largest, in descending
+ * order, are the token's slots.  Logits of -inf and NaN, and choice values of
+ * -inf and NaN, take no part (score 0); where fewer than k experts are left,
+ * the last slots are -1 with weight 0.  Softmax: logits of +inf share all of it.
+ *   logits        [T][E] bf16 or fp32, 16-byte aligned.
+ *   bias          fp32 [E] or NULL; takes part in the choice only.
+ *   live          uint8 [T] or NULL: 0 for tokens that are padding, all of
+ *                 whose slots are -1.
+ *   topk_idx      int32 [T][k];  topk_weights fp32 [T][k]. */
+int ep_router_topk(const moedisp_router* r, const void* logits, const float* bias, const uint8_t* live,
+                   int32_t* topk_idx, float* topk_weights, void* stream);
+
+/* Gradient of the logits from that of the weights; the choice has none.
+ *   topk_idx        as ep_router_topk left it; slots of -1 have no gradient.
+ *   d_topk_weights  fp32 [T][k].
+ *   d_logits        [T][E] in the type of the logits, all written.
+ * An expert that a token names twice gets the sum of both slots, each with its
+ * own weight.  Status bits: BAD_EXPERT_ID (that slot has no gradient). */
+int ep_router_topk_backward(const moedisp_router* r, const void* logits, const int32_t* topk_idx,
+                            const float* d_topk_weights, void* d_logits, void* ws, size_t ws_bytes, void* stream);
 
 /* A batch of num_seqs sequences of seq_len tokens each (token s*seq_len + i
  * is position i of sequence s).  A token all of whose slots are masked (-1)
