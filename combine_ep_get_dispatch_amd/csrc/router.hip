@@ -6,8 +6,9 @@
 // bits hold the index (turned round for c >= 0, so that a lower index is
 // larger): comparing two keys compares values, then indexes, in one
 // instruction, and no two keys are equal.  A binary32 logit has those bits
-// free; scores are computed in 64 bits, and differ by 2^-40 of their value or
-// tie.
+// free; scores are computed in 64 bits and rounded to 41, so that values which
+// are equal but for roundings tie (as the sigmoids of 1 and -1 and twice that
+// of 0, in groups).
 //
 // A row belongs to L lanes, P experts each.  Every lane sorts its keys; then k
 // times the largest of the lanes' first ones is taken, and its lane moves up.
@@ -77,8 +78,7 @@ __device__ inline double lanes_sum64(double v) {
 }
 
 // exp(v) for v <= 0 to about 2^-45: 2^n times the series of the rest, |rest| <
-// 0.35, to the 11th power (the 12th is 6e-15).  Zero below -700; for NaN, an
-// infinite logit less itself, what -700 gives, so that such experts share all.
+// 0.35, to the 11th power (the 12th is 6e-15).  Zero below -700.
 __device__ inline double exp64(double u) {
     const double v = max64(u, -700.0);
     const double n = __builtin_rint(v * 0x1.71547652b82fep+0);
@@ -107,7 +107,7 @@ __device__ inline double rcp64(double v) {
 }
 
 // exp(v) for v <= 0 to about a step of binary32: as 2^h (1 + l ln 2), h + l =
-// v / ln 2.  Zero below -87, where 2^h leaves the normal range; NaN as in exp64.
+// v / ln 2.  Zero below -87, where 2^h leaves the normal range.
 __device__ inline float exp32(float v) {
     const float x = fmaxf(v, -87.0f);
     const float h = x * 0x1.715476p+0f;
@@ -121,9 +121,10 @@ __device__ inline float exp32(float v) {
 constexpr double kNone = -__builtin_huge_val();  // no choice
 constexpr double kTop = 0x1p200;                 // infinity as a value that leaves room for the index
 
-// Value and index as one number.  Only values above kNone.
+// Value, to the nearest of 41 bits, and index as one number.  Only values
+// above kNone.
 __device__ inline double make_key(double c, int e) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, min64(c, kTop) + 0.0);  // -0 becomes 0
+    const uint64_t b = __builtin_bit_cast(uint64_t, min64(c, kTop) + 0.0) + 2048u;  // -0 becomes 0
     const uint64_t at = (int64_t)b < 0 ? (uint64_t)e : (uint64_t)(4095 - e);
     return __builtin_bit_cast(double, (b & ~4095ull) | at);
 }
@@ -155,13 +156,16 @@ __device__ inline void sort_keys(double v[N]) {
 }
 
 template <bool BF16>
-__device__ inline float logit(const void* logits, size_t at) {
+__device__ inline float raw_logit(const void* logits, size_t at) {
     return BF16 ? __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(logits)[at] << 16)
                 : reinterpret_cast<const float*>(logits)[at];
 }
+// +inf counts as the largest finite number, so that differences are numbers;
+// NaN as -inf, which takes no part.
+__device__ inline float tame(float v) { return v == v ? fminf(v, 0x1.fffffep+127f) : -INFINITY; }
 
 // Lane l's logits of a row: experts (c * L + l) * V .. + V - 1 of chunk c, V
-// at a time; -inf past the last expert and for NaN, which take no part.
+// at a time; -inf past the last expert.
 template <int P>
 constexpr int piece() { return P < 8 ? P : 8; }
 template <int L, int P, bool BF16>
@@ -199,11 +203,11 @@ __device__ inline void load_row(const RouterArgs& a, size_t row, int l, float z[
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[c * V + i] = logit<BF16>(a.logits, row * a.E + min(e0 + i, a.E - 1));
+            for (int i = 0; i < V; ++i) z[c * V + i] = raw_logit<BF16>(a.logits, row * a.E + min(e0 + i, a.E - 1));
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            z[c * V + i] = e0 + i < a.E && z[c * V + i] == z[c * V + i] ? z[c * V + i] : -INFINITY;
+            z[c * V + i] = e0 + i < a.E ? tame(z[c * V + i]) : -INFINITY;
     }
 }
 
@@ -350,7 +354,7 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
     for (int h = 0; h < kSlots; ++h) {
         const bool taken = slot[h] > kNone && on;
         e[h] = taken ? key_index(slot[h]) : -1;
-        zs[h] = taken ? logit<BF16>(a.logits, row * a.E + e[h]) : -INFINITY;
+        zs[h] = taken ? tame(raw_logit<BF16>(a.logits, row * a.E + e[h])) : -INFINITY;
         m = fmaxf(m, zs[h]);
     }
     float w[kSlots], all = 0.0f;
@@ -401,7 +405,7 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router_backward(Router
         e[h] = real ? a.topk_idx[row * a.k + j] : -1;
         bad |= e[h] < -1 || e[h] >= a.E;
         if (e[h] >= a.E) e[h] = -1;
-        zs[h] = e[h] >= 0 ? logit<BF16>(a.logits, row * a.E + e[h]) : -INFINITY;
+        zs[h] = e[h] >= 0 ? tame(raw_logit<BF16>(a.logits, row * a.E + e[h])) : -INFINITY;
         if (!(zs[h] > -INFINITY)) e[h] = -1;  // takes no part
         any |= e[h] >= 0;
         g[h] = e[h] >= 0 ? a.scale * a.weights[row * a.k + j] : 0.0f;

@@ -530,7 +530,7 @@ typedef enum {
  *              scales of one group of channels lie together.
  *   y          [max_rows][n] bf16 or fp32 (out_dtype).
  * E2M1: a weight times its scale is taken as bf16 number, infinite beyond its
- * range.  INT4: sums over a group's x times code + 8 are binary32 and at most
+ * range (NaN times an x of 0).  INT4: sums over a group's x times code + 8 are binary32 and at most
  * 5 times as large as those of x times 8, so x has to stay below 2^122; a row
  * that holds an infinity gives NaN.  Rows, bounds, ws, overlap and alignment
  * as said at moedisp_rows (UE8M0 scales: 4 bytes, bf16 scales: 4 bytes).
@@ -562,13 +562,14 @@ typedef struct {
 /* The choice of k experts for each token, and their weights: what dispatch,
  * combine and the balance loss take as topk_idx and topk_weights.
  *   choice value  the logit where there is neither bias nor groups, else
- *                 score + bias, to 2^-40 of its value.
+ *                 score + bias, to the nearest number of 41 bits.
  *   num_groups    above 1: only the topk_groups groups of the largest value
- *                 are chosen from.
+ *                 (to 41 bits) are chosen from.
  * Among equals the lowest index comes first.  The k largest, in descending
  * order, are the token's slots.  Logits of -inf and NaN, and choice values of
  * -inf and NaN, take no part (score 0); where fewer than k experts are left,
- * the last slots are -1 with weight 0.  Softmax: logits of +inf share all of it.
+ * the last slots are -1 with weight 0.  A logit of +inf counts as the largest
+ * finite binary32 number.
  *   logits        [T][E] bf16 or fp32, 16-byte aligned.
  *   bias          fp32 [E] or NULL; takes part in the choice only.
  *   live          uint8 [T] or NULL: 0 for tokens that are padding, all of

@@ -125,6 +125,11 @@ class Bf16Problem:
         return M.ep_check_status(self.ws)
 
 
+def to41(v):
+    """binary64 values to the nearest of 41 bits, as the choice compares them."""
+    return ((v + 0.0).view(torch.int64) + 2048 & ~4095).view(torch.float64)
+
+
 def router64(z, k, score, bias=None, live=None, groups=1, topk_groups=1, group_best=2, normalise=True, scale=1.0):
     """(idx, weights) of logits [T][E] in 64 bits; weights carry the gradient of z."""
     T, E = z.shape
@@ -140,12 +145,14 @@ def router64(z, k, score, bias=None, live=None, groups=1, topk_groups=1, group_b
         key = p.detach().clone() if by_score else zz.detach().clone()
         if bias is not None:
             key = key + bias.double()
+        if by_score:
+            key = torch.where(torch.isfinite(key), to41(key), key)
         key = torch.where(dead | torch.isnan(key), -torch.inf, key)
         if groups > 1:
             v = key.view(T, groups, E // groups).sort(2, descending=True).values[..., :group_best]
             some = v[..., 0] > -torch.inf
             v = torch.where(v > -torch.inf, v, 0.0).sum(2)
-            v = torch.where(some, v, -torch.inf)
+            v = torch.where(some, torch.where(torch.isfinite(v), to41(v), v), -torch.inf)
             order = v.argsort(dim=1, descending=True, stable=True)[:, :topk_groups]
             kept = torch.zeros(T, groups, dtype=torch.bool, device=z.device).scatter_(1, order, True)
             key = torch.where(kept.repeat_interleave(E // groups, 1), key, -torch.inf)
