@@ -253,7 +253,9 @@ hipError_t launch_variant(const ExpertBf16Args& a, int mean_rows, hipStream_t st
     const TileShape t = expert_gemm_bf16_tile(a.r.E, a.n, mean_rows);
     if (t.a == 32) return launch_tile<32, 128, 1, 4, 3, 3, KN, F32>(a, stream);
     if (t.a == 64) return launch_tile<64, 256, 2, 4, 3, 3, KN, F32>(a, stream);
+    if (t.a == 96) return launch_tile<96, 256, 2, 4, 3, 2, KN, F32>(a, stream);
     if (t.a == 128) return launch_tile<128, 256, 2, 4, 3, 2, KN, F32>(a, stream);
+    if (t.a == 160) return launch_tile<160, 256, 2, 4, 3, 2, KN, F32>(a, stream);
     return launch_tile<256, 256, 4, 2, 2, 2, KN, F32>(a, stream);
 }
 
@@ -262,12 +264,15 @@ hipError_t launch_variant(const ExpertBf16Args& a, int mean_rows, hipStream_t st
 TileShape expert_gemm_bf16_tile(int E, int n, int mean_rows) {
     const long long small = (long long)E * (((long long)mean_rows + 31) / 32) * ((n + 127) / 128);
     if (mean_rows <= 16 || small <= 2 * kCus || (mean_rows <= 32 && small <= 4 * kCus)) return {32, 128};
-    if (mean_rows <= 48 || small <= 4 * kCus) return {64, 256};
+    if (mean_rows <= 32 || small <= 4 * kCus) return {64, 256};
+    if (mean_rows <= 72) return {96, 256};
+    if (mean_rows <= 112) return {128, 256};
+    if (mean_rows <= 144) return {160, 256};
     const long long nt = (n + 255) / 256;
     const long long large = E * (((long long)mean_rows + 255) / 256) * nt;
     const long long half = E * (((long long)mean_rows + 127) / 128) * nt;
     const long long rounds = (large + kCus - 1) / kCus * kCus;
-    if (mean_rows <= 144 || rounds * 4 > half * 3) return {128, 256};
+    if (rounds * 4 > half * 3) return {128, 256};
     return {256, 256};
 }
 

@@ -327,6 +327,7 @@ struct SwigluArgs {
 struct RouterArgs {
     int T, E, k;
     int groups, topk_groups, per_group, group_best;
+    int group_lanes;   // neighbouring lanes that share a group
     bool sigmoid, normalise;
     bool vec;          // rows of whole 16-byte (8-byte) pieces
     float scale;

@@ -2,7 +2,8 @@
 //
 // Choice.  An expert's choice value c is its logit, or its score plus bias
 // where a bias or groups take part; a row's k largest are chosen, the lowest
-// index first among equals.  c is kept as a binary64 number whose 12 lowest
+// index first among equals.  A bf16 logit and the index make one integer of 28
+// bits.  Other choice values are kept as a binary64 number whose 12 lowest
 // bits hold the index (turned round for c >= 0, so that a lower index is
 // larger): comparing two keys compares values, then indexes, in one
 // instruction, and no two keys are equal.  A binary32 logit has those bits
@@ -26,6 +27,8 @@
 //     normalised            dz = s (g - sum_i g_i s_i), sigmoid: times 1 - score
 //     softmax               dz = p ([chosen] g - sum_i g_i p_i), all experts
 //     sigmoid               dz = g s (1 - s)
+#include <type_traits>
+
 #include "experts_common.h"
 
 namespace moedisp {
@@ -118,28 +121,73 @@ __device__ inline float exp32(float v) {
     return v < -87.0f ? 0.0f : e;
 }
 
-constexpr double kNone = -__builtin_huge_val();  // no choice
-constexpr double kTop = 0x1p200;                 // infinity as a value that leaves room for the index
-
-// Value, to the nearest of 41 bits, and index as one number.  Only values
-// above kNone.
-__device__ inline double make_key(double c, int e) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, min64(c, kTop) + 0.0) + 2048u;  // -0 becomes 0
-    const uint64_t at = (int64_t)b < 0 ? (uint64_t)e : (uint64_t)(4095 - e);
-    return __builtin_bit_cast(double, (b & ~4095ull) | at);
-}
-__device__ inline int key_index(double key) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, key);
-    const int low = (int)(b & 4095u);
-    return (int64_t)b < 0 ? low : 4095 - low;
-}
-__device__ inline double key_value(double key) {
-    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~4095ull);
-}
+// Keys: value and index as one number that orders by value, then by the lower
+// index.  No two of a row's experts have the same.
+struct Key64 {
+    using type = double;
+    static constexpr double kNone = -__builtin_huge_val();  // no choice
+    // c to the nearest of 41 bits; infinity as 2^200, which leaves room for the
+    // index.  Only values above kNone.
+    static __device__ inline double make(double c, int e) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, min64(c, 0x1p200) + 0.0) + 2048u;  // -0 becomes 0
+        const uint64_t at = (int64_t)b < 0 ? (uint64_t)e : (uint64_t)(4095 - e);
+        return __builtin_bit_cast(double, (b & ~4095ull) | at);
+    }
+    static __device__ inline int index(double key) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, key);
+        const int low = (int)(b & 4095u);
+        return (int64_t)b < 0 ? low : 4095 - low;
+    }
+    static __device__ inline double value(double key) {
+        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~4095ull);
+    }
+    static __device__ inline double larger(double a, double b) { return max64(a, b); }
+    static __device__ inline double smaller(double a, double b) { return min64(a, b); }
+    template <int L>
+    static __device__ inline double largest(double v) { return lanes_max64<L>(v); }
+    // a where the mask is all ones, b where it is zero.  (The compiler would turn
+    // a choice between neighbours of an array into an access by index.)
+    static __device__ inline double pick(uint32_t mask, double a, double b) {
+        const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
+        const uint32_t lo = ((uint32_t)x & mask) | ((uint32_t)y & ~mask);
+        const uint32_t hi = ((uint32_t)(x >> 32) & mask) | ((uint32_t)(y >> 32) & ~mask);
+        return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    }
+};
+// The bits of a bf16 logit, turned so that they order as integers, above the index.
+struct Key32 {
+    using type = uint32_t;
+    static constexpr uint32_t kNone = 0;  // -inf is 0x7F above the index
+    static __device__ inline uint32_t make(float z, int e) {
+        const uint32_t b = __float_as_uint(z + 0.0f) >> 16;  // -0 becomes 0
+        return (b ^ (b & 0x8000u ? 0xFFFFu : 0x8000u)) << 12 | (uint32_t)(4095 - e);
+    }
+    static __device__ inline int index(uint32_t key) { return 4095 - (int)(key & 4095u); }
+    static __device__ inline uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+    static __device__ inline uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
+    template <int L>
+    static __device__ inline uint32_t largest(uint32_t v) {
+        auto moved = [](uint32_t x, auto ctrl) {
+            return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xF, 0xF, true);
+        };
+        v = max(v, moved(v, std::integral_constant<int, 0xB1>{}));
+        v = max(v, moved(v, std::integral_constant<int, 0x4E>{}));
+        v = max(v, moved(v, std::integral_constant<int, 0x141>{}));
+        v = max(v, moved(v, std::integral_constant<int, 0x140>{}));
+        if (L > 16) {
+            auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+            v = max((uint32_t)r[0], (uint32_t)r[1]);
+            r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+            v = max((uint32_t)r[0], (uint32_t)r[1]);
+        }
+        return v;
+    }
+    static __device__ inline uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
+};
 
 // Descending, by Batcher's odd-even merge network.
-template <int N>
-__device__ inline void sort_keys(double v[N]) {
+template <class K, int N>
+__device__ inline void sort_keys(typename K::type v[N]) {
 #pragma unroll
     for (int p = 1; p < N; p <<= 1)
 #pragma unroll
@@ -149,9 +197,9 @@ __device__ inline void sort_keys(double v[N]) {
 #pragma unroll
                 for (int i = 0; i < q; ++i)
                     if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const double x = v[i + j], y = v[i + j + q];
-                        v[i + j] = max64(x, y);
-                        v[i + j + q] = min64(x, y);
+                        const auto x = v[i + j], y = v[i + j + q];
+                        v[i + j] = K::larger(x, y);
+                        v[i + j + q] = K::smaller(x, y);
                     }
 }
 
@@ -224,10 +272,102 @@ __device__ inline float part(bool sigmoid, float z, float m) {
     return exp32(fminf(z, 0.0f) - fminf(m, 0.0f)) / (1.0f + exp32(-fabsf(z)));
 }
 
-template <int L, int P, bool BF16>
+// exp(v) for v <= 0, for sums: off by |v| steps, which the terms' own size
+// makes up for.
+__device__ inline float exp_term(float v) { return __builtin_amdgcn_exp2f(v * 0x1.715476p+0f); }
+
+// Choice values from scores, in 64 bits.  *sum is the softmax's sum.
+template <int L, int P>
+__device__ inline void score_keys(const RouterArgs& a, int l, const float z[P], float top, double key[P], float* sum) {
+    double total = 1.0;
+    if (!a.sigmoid) {
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            key[i] = exp64((double)z[i] - (double)top);
+            total += key[i];
+        }
+        total = lanes_sum64<L>(total);
+        *sum = (float)total;
+        total = rcp64(total);
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int e = expert_of<L, P>(l, i);
+        double c;
+        if (a.sigmoid) {
+            const double zd = (double)z[i];
+            const double x = exp64(-__builtin_fabs(zd));
+            c = (zd < 0.0 ? x : 1.0) * rcp64(1.0 + x);
+        } else {
+            c = key[i] * total;
+        }
+        if (a.bias) c += (double)a.bias[min(e, a.E - 1)];
+        // -inf and NaN, also from the bias, are no choice
+        key[i] = z[i] > -INFINITY && c > Key64::kNone ? Key64::make(c, e) : Key64::kNone;
+    }
+}
+
+// Takes away the experts of groups that are not among the best.  A group's
+// experts, in LDS, belong to a.group_lanes neighbouring lanes.
+template <int L, int P>
+__device__ inline void keep_groups(const RouterArgs& a, int l, double* mine, double key[P]) {
+    constexpr double kNone = Key64::kNone;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int e = expert_of<L, P>(l, i);
+        if (e < a.E) mine[e] = key[i];
+    }
+    __syncthreads();
+    constexpr int kG = kMaxGroups / L;  // passes over the groups, where each has one lane
+    const int at_once = L / a.group_lanes;
+    const int sub = l % a.group_lanes;
+    double group[kG];
+#pragma unroll
+    for (int h = 0; h < kG; ++h) {
+        const int g = h * at_once + l / a.group_lanes;
+        double first = kNone, second = kNone;
+        if (g < a.groups)
+            for (int i = sub; i < a.per_group; i += a.group_lanes) {
+                const double v = mine[g * a.per_group + i];
+                second = max64(second, min64(first, v));
+                first = max64(first, v);
+            }
+        for (int d = 1; d < a.group_lanes; d <<= 1) {
+            const double f = __shfl_xor(first, d), s = __shfl_xor(second, d);
+            second = max64(min64(first, f), max64(second, s));
+            first = max64(first, f);
+        }
+        group[h] = kNone;
+        if (first > kNone && sub == 0) {
+            double v = Key64::value(first);
+            if (a.group_best > 1 && second > kNone) v += Key64::value(second);
+            group[h] = Key64::make(v, g);
+        }
+    }
+    uint64_t kept = 0;
+    for (int j = 0; j < a.topk_groups; ++j) {
+        double best = group[0];
+#pragma unroll
+        for (int h = 1; h < kG; ++h) best = max64(best, group[h]);
+        best = lanes_max64<L>(best);
+        if (best > kNone) kept |= 1ull << Key64::index(best);
+#pragma unroll
+        for (int h = 0; h < kG; ++h) group[h] = group[h] == best ? kNone : group[h];
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int e = min(expert_of<L, P>(l, i), a.E - 1);
+        if (!(kept >> (e / a.per_group) & 1)) key[i] = kNone;
+    }
+}
+
+// K: Key64, or Key32 for the choice by bf16 logits.
+template <class K, int L, int P, bool BF16>
 __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
     constexpr int kRows = kRouterThreads / L;
     constexpr int kSlots = (kMaxSlots + L - 1) / L;  // slots of a lane
+    constexpr bool k64 = std::is_same<K, Key64>::value;
     extern __shared__ __align__(16) double s_keys[];  // groups: [kRows][E]
     const int l = threadIdx.x % L;
     const long long at = (long long)blockIdx.x * kRows + threadIdx.x / L;
@@ -236,124 +376,56 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
 
     float z[P];
     load_row<L, P, BF16>(a, row, l, z);
-    const bool by_score = a.bias != nullptr || a.groups > 1;
+    const bool by_score = k64 && (a.bias != nullptr || a.groups > 1);
     float top = 0.0f, sum = 1.0f;  // softmax: the row's largest logit, the sum of exp(z - top)
-    double key[P];
     if (!a.sigmoid && (by_score || !a.normalise)) {
         top = z[0];
 #pragma unroll
         for (int i = 1; i < P; ++i) top = fmaxf(top, z[i]);
         top = lanes_max<L>(top);
-    }
-    if (by_score) {
-        double total = 1.0;
-        if (!a.sigmoid) {
-            total = 0.0;
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                key[i] = exp64((double)z[i] - (double)top);
-                total += key[i];
-            }
-            total = lanes_sum64<L>(total);
-            sum = (float)total;
-            total = rcp64(total);
-        }
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int e = expert_of<L, P>(l, i);
-            double c;
-            if (a.sigmoid) {
-                const double zd = (double)z[i];
-                const double x = exp64(-__builtin_fabs(zd));
-                c = (zd < 0.0 ? x : 1.0) * rcp64(1.0 + x);
-            } else {
-                c = key[i] * total;
-            }
-            if (a.bias) c += (double)a.bias[min(e, a.E - 1)];
-            // -inf and NaN, also from the bias, are no choice
-            key[i] = z[i] > -INFINITY && c > kNone ? make_key(c, e) : kNone;
-        }
-    } else {
-        if (!a.sigmoid && !a.normalise) {
+        if (!by_score) {
             sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < P; ++i) sum += exp32(z[i] - top);
+            for (int i = 0; i < P; ++i) sum += exp_term(z[i] - top);
             sum = lanes_sum<L>(sum);
         }
+    }
+    typename K::type key[P];
+    if constexpr (k64) {
+        if (by_score) {
+            score_keys<L, P>(a, l, z, top, key, &sum);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                key[i] = z[i] > -INFINITY ? Key64::make((double)z[i], expert_of<L, P>(l, i)) : Key64::kNone;
+        }
+        if (a.groups > 1) keep_groups<L, P>(a, l, s_keys + (size_t)(threadIdx.x / L) * a.E, key);
+    } else {
 #pragma unroll
         for (int i = 0; i < P; ++i)
-            key[i] = z[i] > -INFINITY ? make_key((double)z[i], expert_of<L, P>(l, i)) : kNone;
+            key[i] = z[i] > -INFINITY ? Key32::make(z[i], expert_of<L, P>(l, i)) : Key32::kNone;
     }
 
-    if (a.groups > 1) {
-        // a lane finds the best values of its groups, in LDS; lanes start at
-        // different experts so that they meet different banks
-        double* const mine = s_keys + (size_t)(threadIdx.x / L) * a.E;
+    sort_keys<K, P>(key);
+    typename K::type slot[kSlots];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int e = expert_of<L, P>(l, i);
-            if (e < a.E) mine[e] = key[i];
-        }
-        __syncthreads();
-        constexpr int kG = kMaxGroups / L;
-        double group[kG];
-#pragma unroll
-        for (int h = 0; h < kG; ++h) {
-            const int g = h * L + l;
-            group[h] = kNone;
-            if (g < a.groups) {
-                double first = kNone, second = kNone;
-                int at_e = g % a.per_group;
-                for (int i = 0; i < a.per_group; ++i) {
-                    const double v = mine[g * a.per_group + at_e];
-                    second = max64(second, min64(first, v));
-                    first = max64(first, v);
-                    at_e = at_e + 1 == a.per_group ? 0 : at_e + 1;
-                }
-                if (first > kNone) {
-                    double v = key_value(first);
-                    if (a.group_best > 1 && second > kNone) v += key_value(second);
-                    group[h] = make_key(v, g);
-                }
-            }
-        }
-        uint64_t kept = 0;
-        for (int j = 0; j < a.topk_groups; ++j) {
-            double best = group[0];
-#pragma unroll
-            for (int h = 1; h < kG; ++h) best = max64(best, group[h]);
-            best = lanes_max64<L>(best);
-            if (best > kNone) kept |= 1ull << key_index(best);
-#pragma unroll
-            for (int h = 0; h < kG; ++h) group[h] = group[h] == best ? kNone : group[h];
-        }
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int e = min(expert_of<L, P>(l, i), a.E - 1);
-            if (!(kept >> (e / a.per_group) & 1)) key[i] = kNone;
-        }
-    }
-
-    sort_keys<P>(key);
-    double slot[kSlots];
-#pragma unroll
-    for (int h = 0; h < kSlots; ++h) slot[h] = kNone;
+    for (int h = 0; h < kSlots; ++h) slot[h] = K::kNone;
     for (int j = 0; j < a.k; ++j) {
-        const double best = lanes_max64<L>(key[0]);
+        const auto best = K::template largest<L>(key[0]);
 #pragma unroll
         for (int h = 0; h < kSlots; ++h) slot[h] = j == h * L + l ? best : slot[h];
-        const bool won = key[0] == best;
+        const uint32_t won = key[0] == best ? 0xFFFFFFFFu : 0u;
 #pragma unroll
-        for (int i = 0; i + 1 < P; ++i) key[i] = won ? key[i + 1] : key[i];
-        key[P - 1] = won ? kNone : key[P - 1];
+        for (int i = 0; i + 1 < P; ++i) key[i] = K::pick(won, key[i + 1], key[i]);
+        key[P - 1] = K::pick(won, K::kNone, key[P - 1]);
     }
 
     int e[kSlots];
     float zs[kSlots], m = -INFINITY;
 #pragma unroll
     for (int h = 0; h < kSlots; ++h) {
-        const bool taken = slot[h] > kNone && on;
-        e[h] = taken ? key_index(slot[h]) : -1;
+        const bool taken = slot[h] > K::kNone && on;
+        e[h] = taken ? K::index(slot[h]) : -1;
         zs[h] = taken ? tame(raw_logit<BF16>(a.logits, row * a.E + e[h])) : -INFINITY;
         m = fmaxf(m, zs[h]);
     }
@@ -507,8 +579,16 @@ hipError_t launch_shape(RouterArgs a, bool backward, hipStream_t stream) {
         hipLaunchKernelGGL((moedisp_router_backward<L, P, BF16>), dim3((unsigned)blocks), dim3(kRouterThreads), 0,
                            stream, a);
     } else {
+        const bool logits_only = a.bias == nullptr && a.groups == 1;
         const size_t lds = a.groups > 1 ? (size_t)kRows * a.E * sizeof(double) : 0;
-        hipLaunchKernelGGL((moedisp_router<L, P, BF16>), dim3((unsigned)blocks), dim3(kRouterThreads), lds, stream, a);
+        a.group_lanes = 1;
+        while (2 * a.group_lanes * a.groups <= L) a.group_lanes *= 2;
+        if (BF16 && logits_only)
+            hipLaunchKernelGGL((moedisp_router<Key32, L, P, true>), dim3((unsigned)blocks), dim3(kRouterThreads), 0,
+                               stream, a);
+        else
+            hipLaunchKernelGGL((moedisp_router<Key64, L, P, BF16>), dim3((unsigned)blocks), dim3(kRouterThreads), lds,
+                               stream, a);
     }
     return hipGetLastError();
 }
