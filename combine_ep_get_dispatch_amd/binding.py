@@ -309,6 +309,12 @@ _INT32 = (torch.int32,)
 _BYTES = None  # any element type (workspaces, probe buffers)
 
 
+# the handle of a GPU's current stream, without an object around it (0.1 us
+# instead of 1.1)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class _Args:
     """Checks of the tensor arguments of one call, before any pointer crosses
     the C ABI: each tensor must have an accepted element type, be contiguous
@@ -320,7 +326,7 @@ class _Args:
 
     def __init__(self, call: str):
         self.call = call
-        self.tensors, self.read, self.out = [], [], []
+        self.tensors, self.read, self.out = [], [], []  # by need(); by arg(): read, written
 
     def fail(self, msg: str):
         raise MoeDispError(self.call, ERR_INVALID_ARG, msg)
@@ -350,18 +356,13 @@ class _Args:
     def arg(self, name: str, t, dtypes, nbytes: int, optional: bool = False, written: bool = False):
         """As need(); returns the tensor's address (None for none).  The call
         writes to a tensor that is `written`."""
-        if type(t) is torch.Tensor and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
-            have = t.nbytes
-            if have < nbytes:
-                self.need(name, t, dtypes, nbytes, optional)  # says so
-            self.tensors.append((name, t, have))
-        else:
+        if type(t) is not torch.Tensor or (dtypes is not None and t.dtype not in dtypes) or not t.is_contiguous() \
+                or t.nbytes < nbytes:
             self.need(name, t, dtypes, nbytes, optional)  # takes a subclass or none, else says what is wrong
             if t is None:
                 return None
-            have = t.nbytes
         at = t.data_ptr()
-        (self.out if written else self.read).append((at, at + have, name))
+        (self.out if written else self.read).append((at, at + t.nbytes, name, t))
         return at
 
     def on_device(self, stream):
@@ -370,20 +371,24 @@ class _Args:
         memory with any other.  Returns the GPU's index and the stream's
         handle (its current stream unless one is given), so that the call does
         not depend on which device is current."""
-        dev = self.tensors[0][1].get_device()
+        every = self.read + self.out
+        dev = every[0][3].get_device()
         same = dev >= 0
-        for _, t, _ in self.tensors:
-            if t.get_device() != dev:
+        for a in every:
+            if a[3].get_device() != dev:
                 same = False
-        for i, (at, end, name) in enumerate(self.out):
-            for oat, oend, other in self.read + self.out[i + 1:]:
+        left = len(self.read)
+        for at, end, name, _ in self.out:
+            left += 1
+            for oat, oend, other, _ in self.read + self.out[left - len(self.read):]:
                 if at < oend and oat < end:
                     self.fail(f"{name} overlaps {other}")
         if not same:
+            self.tensors = [(n, t, t.nbytes) for _, _, n, t in every]
             self.done()
             self.fail("the tensors lie on different GPUs: " + ", ".join(f"{n} on {t.device}" for n, t, _ in self.tensors))
         if stream is None:
-            return dev, torch.cuda.current_stream(dev).cuda_stream
+            return dev, _raw_stream(dev)
         if stream.device.index != dev:
             self.fail(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
         return dev, stream.cuda_stream

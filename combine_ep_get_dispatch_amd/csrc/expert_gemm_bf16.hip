@@ -34,15 +34,16 @@ struct Tile {
     static constexpr int kNT = kN / 16;
     static constexpr int kWLoads = BN / 8 / kWaves;  // 1 KiB loads of a wave and step
     static constexpr int kXLoads = (BM / 8 + kWaves - 1) / kWaves;
-    // Loads of a wave and step, in this order: the rows of step kb + XS, the
-    // weights of step kb + WS.  Before step kb + 1 its rows have to be there,
-    // and all that is older; what is younger may be under way.
+    // Loads of a wave and step kb, in this order: the rows of step kb + XS, as
+    // soon as those of step kb are in registers; the weights of step kb + WS,
+    // behind the last of step kb.  Before step kb + 1 its own have to be there;
+    // younger ones may be under way.
     static constexpr int kLoads = kWLoads + kXLoads;
-    static constexpr int kYounger = (WS > XS ? kWLoads : 0) + (XS - 2) * kLoads;
+    static constexpr int kYounger = (XS - 1) * kXLoads + (WS - 2) * kWLoads;
     static constexpr int kXBytes = kXLoads * kWaves * 1024;
     static constexpr int kWStage = BN * 2 * kBlk;
     static constexpr int kLds = WS * kWStage + XS * kXBytes;
-    static_assert(WS >= XS && XS >= 2 && WS - XS <= 1, "stages");
+    static_assert(WS >= XS && XS >= 2 && WS - XS <= 1 && (WS + XS) * kLoads < 64, "stages");
     static_assert(kNT % 2 == 0 && kM % 16 == 0 && kN % 32 == 0 && BN % (8 * kWaves) == 0 && BN >= 128, "tile shape");
     static_assert(kLds <= kLdsBytes, "LDS");
 };
@@ -172,14 +173,14 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
         auto x_at = [&](const char* st, int j) { return read_rows(st + (xrow + j * 16) * 128, xsw); };
 
         Frag b[T::kMT], wf[2];
-        wait_loads_and_sync<T::kYounger + T::kLoads>();
+        wait_loads_and_sync<(XS - 1) * T::kXLoads + (WS - 1) * T::kWLoads>();
         wf[0] = w_at(lds, 0);
 #pragma unroll
         for (int j = 0; j < T::kMT; ++j) b[j] = x_at(x_lds, j);
         // Step kb: its rows' operands and the first of the weights' are in
-        // registers.  Before the last i the step's LDS has been read: the waves
-        // meet, its place is filled with the step stages later, and the next
-        // step's operands are read behind the last products.
+        // registers.  Behind the first products the waves meet, as all have read
+        // the rows, whose place is filled; before the last ones again, for the
+        // weights; the next step's operands are read behind the last products.
         int wbuf = 0, xbuf = 0;
         for (int kb = 0; kb < steps; ++kb) {
             const char* st = lds + wbuf * T::kWStage;
@@ -192,7 +193,6 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
                 if (i + 1 < T::kNT) wf[(i + 1) & 1] = w_at(st, i + 1);
                 if (i == T::kNT - 1) {
                     wait_loads_and_sync<T::kYounger>();
-                    issue_x(kb + XS, xbuf);
                     issue_w(kb + WS, wbuf);
                     __builtin_amdgcn_sched_barrier(0);
                     wf[0] = w_at(nst, 0);
@@ -202,6 +202,11 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1].lo, b[j].lo, acc[i][j], 0, 0, 0);
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1].hi, b[j].hi, acc[i][j], 0, 0, 0);
                     if (i == T::kNT - 1) b[j] = x_at(nxt, j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (i == 0) {
+                    reads_done_and_sync();
+                    issue_x(kb + XS, xbuf);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
