@@ -109,24 +109,20 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
         const int wm = wave % WM, wn = wave / WM;
         char* const x_lds = lds + WS * T::kWStage;
 
-        // steps past the last load the last one again, to no use
-        auto issue_w = [&](int kb, int buf) {
+        // load i of step kb; steps past the last load the last one again, to no use
+        auto issue_w = [&](int kb, int buf, int i) {
             const int s = min(kb, steps - 1);
             const char* const base = wp + (KN ? (size_t)s * kBlk * a.n * 2 : (size_t)s * kBlk * 2);
             const uint32_t out = s == steps - 1 ? w_out : 0u;
-#pragma unroll
-            for (int i = 0; i < T::kWLoads; ++i)
-                load_to_lds_unseen<16>(base, lds + buf * T::kWStage + (wave * T::kWLoads + i) * 1024,
-                                       out >> i & 1 ? kOutside : woff[i]);
+            load_to_lds_unseen<16>(base, lds + buf * T::kWStage + (wave * T::kWLoads + i) * 1024,
+                                   out >> i & 1 ? kOutside : woff[i]);
         };
-        auto issue_x = [&](int kb, int buf) {
+        auto issue_x = [&](int kb, int buf, int i) {
             const int s = min(kb, steps - 1);
             const char* const base = xp + (size_t)s * kBlk * 2;
             const uint32_t out = s == steps - 1 ? x_out : 0u;
-#pragma unroll
-            for (int i = 0; i < T::kXLoads; ++i)
-                load_to_lds_unseen<16>(base, x_lds + buf * T::kXBytes + (wave * T::kXLoads + i) * 1024,
-                                       out >> i & 1 ? kOutside : xoff[i]);
+            load_to_lds_unseen<16>(base, x_lds + buf * T::kXBytes + (wave * T::kXLoads + i) * 1024,
+                                   out >> i & 1 ? kOutside : xoff[i]);
         };
 
         v4f acc[T::kNT][T::kMT];
@@ -137,8 +133,11 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
 
 #pragma unroll
         for (int p = 0; p < WS; ++p) {
-            if (p >= WS - XS) issue_x(p - (WS - XS), p - (WS - XS));
-            issue_w(p, p);
+#pragma unroll
+            for (int i = 0; i < T::kXLoads; ++i)
+                if (p >= WS - XS) issue_x(p - (WS - XS), p - (WS - XS), i);
+#pragma unroll
+            for (int i = 0; i < T::kWLoads; ++i) issue_w(p, p, i);
             __builtin_amdgcn_sched_barrier(0);
         }
 
@@ -193,8 +192,6 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
                 if (i + 1 < T::kNT) wf[(i + 1) & 1] = w_at(st, i + 1);
                 if (i == T::kNT - 1) {
                     wait_loads_and_sync<T::kYounger>();
-                    issue_w(kb + WS, wbuf);
-                    __builtin_amdgcn_sched_barrier(0);
                     wf[0] = w_at(nst, 0);
                 }
 #pragma unroll
@@ -203,10 +200,26 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_bf16(ExpertB
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1].hi, b[j].hi, acc[i][j], 0, 0, 0);
                     if (i == T::kNT - 1) b[j] = x_at(nxt, j);
                     __builtin_amdgcn_sched_barrier(0);
+                    // the loads one by one between the products
+                    constexpr int kPlaces = (T::kNT - 2) * T::kMT;
+                    if (i > 0 && i < T::kNT - 1) {
+                        const int place = (i - 1) * T::kMT + j;
+#pragma unroll
+                        for (int l = 0; l < T::kXLoads; ++l)
+                            if (l * kPlaces / T::kXLoads == place) issue_x(kb + XS, xbuf, l);
+                    }
+                    if (i == T::kNT - 1) {
+#pragma unroll
+                        for (int l = 0; l < T::kWLoads; ++l)
+                            if (l * T::kMT / T::kWLoads == j) issue_w(kb + WS, wbuf, l);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 if (i == 0) {
                     reads_done_and_sync();
-                    issue_x(kb + XS, xbuf);
+#pragma unroll
+                    for (int l = 0; l < T::kXLoads; ++l)
+                        if (T::kNT == 2) issue_x(kb + XS, xbuf, l);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }

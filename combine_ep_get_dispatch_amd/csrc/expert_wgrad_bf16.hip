@@ -169,29 +169,45 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
         wait_loads_and_sync<0>();  // no load may reach LDS after the workgroup's end
     }
 
+    // Results by way of LDS, a wave's 16 columns at a time in a place of its
+    // own, so that rows of dw are written in runs of a wave's channels.
+    constexpr int kEl = F32 ? 4 : 2;
+    constexpr int kRunBytes = TK / WK * kEl;   // bytes
+    constexpr int kPitch = kRunBytes + 16;     // rows of 16 lanes start at different banks
+    constexpr int kLanes = kRunBytes / 16;     // lanes of a run
+    static_assert(16 * kPitch * T::kWaves <= T::kLds && 64 % kLanes == 0, "results fit LDS");
+    char* const mine = lds + wave * (16 * kPitch);
 #pragma unroll
     for (int j = 0; j < T::kNT; ++j) {
-        const int n = n0 + wn + j * 16 + c;
-        if (n >= a.n) continue;
-        if (F32) {
 #pragma unroll
-            for (int i = 0; i < T::kKT; ++i) {
-                const int k = k0 + wk + i * 16 + q * 4;
-                if (k >= a.k) continue;
-                v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + ((size_t)e * a.n + n) * a.k + k);
-                *o = ADD ? acc[i][j] + *o : acc[i][j];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < T::kKT; i += 2) {
-                const int k = k0 + wk + i * 16 + q * 8;
-                if (k >= a.k) continue;
+        for (int i = 0; i < T::kKT; i += F32 ? 1 : 2) {
+            char* const to = mine + c * kPitch + (i * 16 + q * (F32 ? 4 : 8)) * kEl;
+            if (F32) {
+                *reinterpret_cast<v4f*>(to) = acc[i][j];
+            } else {
                 const v4f lo = acc[i][j], hi = acc[i + 1][j];
-                *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.y) + ((size_t)e * a.n + n) * a.k + k) =
-                    v4u{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
-                        pack_bf16x2(hi[2], hi[3])};
+                *reinterpret_cast<v4u*>(to) = v4u{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
+                                                  pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])};
             }
         }
+        own_lds_done();
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += 64 / kLanes) {
+            const int r = r0 + lane / kLanes;
+            const int n = n0 + wn + j * 16 + r, k = k0 + wk + lane % kLanes * (16 / kEl);
+            const char* const from = mine + r * kPitch + lane % kLanes * 16;
+            if (n < a.n && k < a.k) {
+                const size_t at = ((size_t)e * a.n + n) * a.k + k;
+                if (F32) {
+                    v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at);
+                    const v4f v = *reinterpret_cast<const v4f*>(from);
+                    *o = ADD ? v + *o : v;
+                } else {
+                    *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.y) + at) = *reinterpret_cast<const v4u*>(from);
+                }
+            }
+        }
+        own_lds_done();
     }
 }
 

@@ -133,6 +133,9 @@ __device__ inline void wait_loads_and_sync() {
 // The workgroup's LDS reads are done; loads may be under way.
 __device__ inline void reads_done_and_sync() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// The wave's own LDS accesses are done.
+__device__ inline void own_lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // At most N of the wave's own loads are under way.
 template <int N>
 __device__ inline void wait_own_loads() {

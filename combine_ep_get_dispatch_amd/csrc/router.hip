@@ -362,6 +362,21 @@ __device__ inline void keep_groups(const RouterArgs& a, int l, double* mine, dou
     }
 }
 
+// The k largest of a row's lanes' sorted keys, slot h * L + l in slot[h] of lane
+// l.  D: entries of a lane that can be among them.
+template <class K, int L, int P, int D>
+__device__ inline void take(int k, int l, typename K::type key[P], typename K::type slot[(kMaxSlots + L - 1) / L]) {
+    for (int j = 0; j < k; ++j) {
+        const auto best = K::template largest<L>(key[0]);
+#pragma unroll
+        for (int h = 0; h < (kMaxSlots + L - 1) / L; ++h) slot[h] = j == h * L + l ? best : slot[h];
+        const uint32_t won = key[0] == best ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+        for (int i = 0; i + 1 < D; ++i) key[i] = K::pick(won, key[i + 1], key[i]);
+        key[D - 1] = K::pick(won, K::kNone, key[D - 1]);
+    }
+}
+
 // K: Key64, or Key32 for the choice by bf16 logits.
 template <class K, int L, int P, bool BF16>
 __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
@@ -410,20 +425,18 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
     typename K::type slot[kSlots];
 #pragma unroll
     for (int h = 0; h < kSlots; ++h) slot[h] = K::kNone;
-    for (int j = 0; j < a.k; ++j) {
-        const auto best = K::template largest<L>(key[0]);
-#pragma unroll
-        for (int h = 0; h < kSlots; ++h) slot[h] = j == h * L + l ? best : slot[h];
-        const uint32_t won = key[0] == best ? 0xFFFFFFFFu : 0u;
-#pragma unroll
-        for (int i = 0; i + 1 < P; ++i) key[i] = K::pick(won, key[i + 1], key[i]);
-        key[P - 1] = K::pick(won, K::kNone, key[P - 1]);
-    }
+    if (P > 8 && a.k <= 8)
+        take<K, L, P, (P < 8 ? P : 8)>(a.k, l, key, slot);
+    else
+        take<K, L, P, (P < kMaxSlots ? P : kMaxSlots)>(a.k, l, key, slot);
 
     int e[kSlots];
     float zs[kSlots], m = -INFINITY;
 #pragma unroll
     for (int h = 0; h < kSlots; ++h) {
+        e[h] = -1;
+        zs[h] = -INFINITY;
+        if (h * L >= a.k) continue;
         const bool taken = slot[h] > K::kNone && on;
         e[h] = taken ? K::index(slot[h]) : -1;
         zs[h] = taken ? tame(raw_logit<BF16>(a.logits, row * a.E + e[h])) : -INFINITY;
@@ -436,6 +449,8 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
         m = a.sigmoid ? 0.0f : top;
 #pragma unroll
     for (int h = 0; h < kSlots; ++h) {
+        w[h] = 0.0f;
+        if (h * L >= a.k) continue;
         w[h] = e[h] >= 0 ? part(a.sigmoid, zs[h], m) : 0.0f;
         all += w[h];
     }
