@@ -6,11 +6,10 @@
 //
 // Precision.  E2M1: a weight times its scale is a bf16 number, made by the
 // conversion instruction; products are exact and sums binary32.  Integers:
-// code q becomes the bf16 number 1 + q/16 by two bit operations a pair, its
-// product with x is exact, and 1.5 times the sum of x, from one more matrix
-// instruction with constant weights, is taken away from a group's sum, which
-// leaves (q - 8)/16; the scale comes last, in binary32.  The detour adds sums
-// up to 5 times as large as the wanted ones.
+// codes 0 .. 15 become bf16 numbers, whose products with x are exact; a group's
+// sum starts at -8 times that of x, from matrix instructions with constant
+// weights; the scale comes last, in binary32.  The detour adds sums up to 3
+// times as large as the wanted ones.
 //
 // How.  A workgroup computes a tile of BM rows by BN columns, KS channels a
 // stage; codes, rows and scales go straight into LDS.  A lane of the matrix
@@ -19,6 +18,8 @@
 // its channels are 32 (lane / 16) + 8 d .. + 7, and the rows' operands are read
 // to match.  A lane's 32 channels are one group of E2M1 weights, the four
 // lanes' 128 one of the integers.
+#include <math.h>
+
 #include "experts_common.h"
 
 namespace moedisp {
@@ -75,18 +76,16 @@ __device__ inline v8bf widen_e2m1(uint32_t v, float s) {
     const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 3);
     return v8bf{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
-// 8 integer codes q as 1 + q/16, in the order 0, 4, 1, 5, 2, 6, 3, 7.
+// 8 codes q = 0 .. 15 as numbers: E4M3 codes 0 .. 15 are q 2^-9, its smallest
+// numbers.
 __device__ inline v8bf widen_int4(uint32_t v) {
-    const v4u o = {((v << 3) & 0x00780078u) | 0x3F803F80u, ((v >> 1) & 0x00780078u) | 0x3F803F80u,
-                   ((v >> 5) & 0x00780078u) | 0x3F803F80u, ((v >> 9) & 0x00780078u) | 0x3F803F80u};
-    return __builtin_bit_cast(v8bf, o);
-}
-// 8 channels in that order.
-__device__ inline v8bf match_int4(v8bf x) {
-    const v4u v = __builtin_bit_cast(v4u, x);
-    const v4u o = {__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
-                   __builtin_amdgcn_perm(v[3], v[1], 0x05040100u), __builtin_amdgcn_perm(v[3], v[1], 0x07060302u)};
-    return __builtin_bit_cast(v8bf, o);
+    const uint32_t even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = __builtin_amdgcn_perm(odd, even, 0x05010400u), hi = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    const v2bf a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false);
+    const v2bf b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true);
+    const v2bf c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false);
+    const v2bf d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true);
+    return v8bf{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
 template <int BM, int BN, int WM, int WN, int KS, int WS, int FMT, bool F32>
@@ -194,56 +193,71 @@ __global__ __launch_bounds__(64 * WM * WN) void moedisp_expert_gemm_w4(ExpertW4A
 #pragma unroll
             for (int h = 0; h < T::kH; ++h) {
                 v4u wf[T::kNT];
-                float sf[T::kNT];
-                v4f part[T::kNT][T::kMT], base[T::kMT];
 #pragma unroll
-                for (int i = 0; i < T::kNT; ++i) {
+                for (int i = 0; i < T::kNT; ++i)
                     wf[i] = *reinterpret_cast<const v4u*>(st + col_of(i) * T::kWRow + (((q + 4 * h) ^ wsw) << 4));
-                    if (T::kE2m1)
-                        sf[i] = __uint_as_float(
-                            (uint32_t) * reinterpret_cast<const uint8_t*>(sc + (q + 4 * h) * T::kN + col + col_of(i))
-                            << 23);
-                }
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    v8bf w[T::kNT];
+                auto x_at = [&](int j, int d) {
+                    const int chunk = ((q + 4 * h) * 4 + d) ^ xsw;
+                    return *reinterpret_cast<const v8bf*>(xt + j * 16 * T::kXRow + (chunk << 4));
+                };
+                if constexpr (T::kE2m1) {
+                    float s[T::kNT];
 #pragma unroll
                     for (int i = 0; i < T::kNT; ++i)
-                        w[i] = T::kE2m1 ? widen_e2m1(wf[i][d], sf[i]) : widen_int4(wf[i][d]);
+                        s[i] = __uint_as_float(
+                            (uint32_t) * reinterpret_cast<const uint8_t*>(sc + (q + 4 * h) * T::kN + col + col_of(i))
+                            << 23);
 #pragma unroll
-                    for (int j = 0; j < T::kMT; ++j) {
-                        const int chunk = ((q + 4 * h) * 4 + d) ^ xsw;
-                        v8bf x = *reinterpret_cast<const v8bf*>(xt + j * 16 * T::kXRow + (chunk << 4));
-                        if constexpr (T::kE2m1) {
+                    for (int d = 0; d < 4; ++d) {
+                        v8bf w[T::kNT];
+#pragma unroll
+                        for (int i = 0; i < T::kNT; ++i) w[i] = widen_e2m1(wf[i][d], s[i]);
+#pragma unroll
+                        for (int j = 0; j < T::kMT; ++j) {
+                            const v8bf x = x_at(j, d);
 #pragma unroll
                             for (int i = 0; i < T::kNT; ++i)
                                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x, acc[i][j], 0, 0, 0);
-                        } else {
-                            x = match_int4(x);
-                            const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                            const v4u k15 = {0xBFC0BFC0u, 0xBFC0BFC0u, 0xBFC0BFC0u, 0xBFC0BFC0u};  // -1.5
-                            base[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k15), x,
-                                                                              d ? base[j] : zero, 0, 0, 0);
-#pragma unroll
-                            for (int i = 0; i < T::kNT; ++i)
-                                part[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], x, d ? part[i][j] : zero, 0,
-                                                                                     0, 0);
                         }
                     }
-                }
-                if constexpr (!T::kE2m1) {
+                } else {
+                    // the scales of the lane's four columns
+                    float s[T::kNT][4];
+                    v8bf w[T::kNT][4];
 #pragma unroll
                     for (int i = 0; i < T::kNT; ++i) {
-                        // the scales of the lane's four columns
                         const v2i sv = *reinterpret_cast<const v2i*>(
                             sc + (h * T::kN + q * (F32 ? 4 : 8) + col_of(i)) * 2);
-                        const float s[4] = {16.0f * bf16_low((uint32_t)sv.x), 16.0f * bf16_high((uint32_t)sv.x),
-                                            16.0f * bf16_low((uint32_t)sv.y), 16.0f * bf16_high((uint32_t)sv.y)};
+                        s[i][0] = bf16_low((uint32_t)sv.x);
+                        s[i][1] = bf16_high((uint32_t)sv.x);
+                        s[i][2] = bf16_low((uint32_t)sv.y);
+                        s[i][3] = bf16_high((uint32_t)sv.y);
 #pragma unroll
-                        for (int j = 0; j < T::kMT; ++j)
+                        for (int d = 0; d < 4; ++d) w[i][d] = widen_int4(wf[i][d]);
+                    }
+                    const v4u k8 = {0xC100C100u, 0xC100C100u, 0xC100C100u, 0xC100C100u};  // -8
+                    const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < T::kMT; ++j) {
+                        v8bf x[4];
+                        v4f base, part[T::kNT];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            x[d] = x_at(j, d);
+                            base = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, k8), x[d],
+                                                                           d ? base : zero, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+#pragma unroll
+                            for (int i = 0; i < T::kNT; ++i)
+                                part[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i][d], x[d], d ? part[i] : base, 0, 0,
+                                                                                  0);
+#pragma unroll
+                        for (int i = 0; i < T::kNT; ++i)
 #pragma unroll
                             for (int v = 0; v < 4; ++v)
-                                acc[i][j][v] = __builtin_fmaf(s[v], part[i][j][v] + base[j][v], acc[i][j][v]);
+                                acc[i][j][v] = __builtin_fmaf(s[i][v], part[i][v], acc[i][j][v]);
                     }
                 }
             }
@@ -291,19 +305,58 @@ hipError_t launch_tile(ExpertW4Args a, hipStream_t stream) {
 
 template <int FMT, bool F32>
 hipError_t launch_variant(const ExpertW4Args& a, int mean_rows, hipStream_t stream) {
-    const TileShape t = expert_gemm_w4_tile(a.r.E, a.n, mean_rows);
+    const TileShape t = expert_gemm_w4_tile(a.r.E, a.n, mean_rows, FMT);
     if (t.a == 16) return launch_tile<16, 128, 1, 4, 256, 3, FMT, F32>(a, stream);
-    if (t.a == 64) return launch_tile<64, 128, 2, 4, 256, 3, FMT, F32>(a, stream);
-    return launch_tile<128, 256, 2, 4, 128, 3, FMT, F32>(a, stream);
+    if (t.a == 32) return launch_tile<32, 256, 1, 4, 128, 3, FMT, F32>(a, stream);
+    if (t.a == 64) return launch_tile<64, 128, 2, 2, 128, 2, FMT, F32>(a, stream);
+    if (t.a == 96) return launch_tile<96, 256, 2, 4, 128, 3, FMT, F32>(a, stream);
+    return launch_tile<160, 256, 2, 4, 128, 2, FMT, F32>(a, stream);
 }
 
 }  // namespace
 
-TileShape expert_gemm_w4_tile(int E, int n, int mean_rows) {
-    const long long mid = (long long)E * (((long long)mean_rows + 63) / 64) * ((n + 127) / 128);
-    if (mean_rows <= 16) return {16, 128};
-    if (mean_rows <= 64 || mid <= kCus) return {64, 128};
-    return {128, 256};
+// The tile whose rounds take the least time.  Experts' rows are taken to
+// scatter round the usual number as random choices do, by its square root.  A
+// round of all compute units takes, for 4096 channels (us; 16 x 128, 32 x 256
+// and 64 x 128 have two workgroups to a unit and go on into the next round, the
+// others start together):
+//              16x128  32x256  64x128  96x256  160x256
+//     E2M1         22      48      38      48       69
+//     integers     24      56      52      63       90
+// 8 experts, K = 4096, integers, us for usual rows (columns):
+//     rows (n)    16x128  32x256  64x128  96x256  160x256
+//       16 (8192)     39      38      52      62       87
+//       32 (8192)     53      53      52      62       87
+//       64 (8192)     93      70      76      64       89
+//      125 (8192)    177     118     118     121       91
+//      125 (8208)    190     117     117     175      171
+//     1024 (8192)   1343     804     802     709      607
+TileShape expert_gemm_w4_tile(int E, int n, int mean_rows, int w4_fmt) {
+    struct Kind {
+        int rows, cols, at_once;
+        double us[2];
+    };
+    static const Kind kinds[] = {{16, 128, 2 * kCus, {22, 24}}, {32, 256, 2 * kCus, {48, 56}},
+                                 {64, 128, 2 * kCus, {38, 52}}, {96, 256, kCus, {48, 63}},
+                                 {160, 256, kCus, {69, 90}}};
+    const double mean = mean_rows, spread = 2.0 * sqrt(mean);
+    TileShape best = {16, 128};
+    double least = 0.0;
+    for (const Kind& k : kinds) {
+        // row tiles of an expert: one more for each multiple of the tile that is exceeded
+        const double whole = floor(fmax(mean - spread, 0.0) / k.rows);
+        double row_tiles = 1.0 + whole;
+        for (double m = whole + 1.0; m * k.rows < mean + spread; m += 1.0)
+            row_tiles += fmin(1.0, fmax(0.0, (mean - m * k.rows) / spread + 0.5));
+        double rounds = row_tiles * E * ((n + k.cols - 1) / k.cols) / k.at_once;
+        rounds = k.at_once > kCus ? fmax(rounds, 1.0) : ceil(rounds);
+        const double us = rounds * k.us[w4_fmt == MOEDISP_W4_INT4];
+        if (k.rows == 16 || us < least) {
+            best = {k.rows, k.cols};
+            least = us;
+        }
+    }
+    return best;
 }
 
 hipError_t launch_expert_gemm_w4(const ExpertW4Args& a, int mean_rows, int w4_fmt, bool f32_out, hipStream_t stream) {

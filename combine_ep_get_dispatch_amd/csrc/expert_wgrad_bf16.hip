@@ -14,11 +14,12 @@ namespace moedisp {
 namespace {
 
 constexpr int kStep = 32;   // rows per step: the contraction of one matrix instruction
-constexpr int kStages = 4;  // steps under way or in use
 
-// Tile of TN columns of dy by TK channels of x; WN x WK waves.
-template <int TN, int TK, int WN, int WK>
+// Tile of TN columns of dy by TK channels of x; WN x WK waves; NS steps under
+// way or in use.
+template <int TN, int TK, int WN, int WK, int NS>
 struct WTile {
+    static constexpr int kStages = NS;
     static constexpr int kWaves = WN * WK;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int kNT = TN / WN / 16;  // 16-wide tiles of a wave
@@ -35,9 +36,10 @@ struct WTile {
                   "tile shape");
 };
 
-template <int TN, int TK, int WN, int WK, bool F32, bool ADD>
+template <int TN, int TK, int WN, int WK, int NS, bool F32, bool ADD>
 __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(ExpertBf16Args a) {
-    using T = WTile<TN, TK, WN, WK>;
+    using T = WTile<TN, TK, WN, WK, NS>;
+    constexpr int kStages = NS;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -170,11 +172,18 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
     }
 
     // Results by way of LDS, a wave's 16 columns at a time in a place of its
-    // own, so that rows of dw are written in runs of a wave's channels.
+    // own, so that rows of dw are written in runs of a wave's channels.  Runs of
+    // whole lines of 128 bytes leave the caches at once (64 experts of 7168 x
+    // 2048, fp32: 693 us, 862 with plain stores); rows that start inside a line
+    // have runs that meet there, where plain stores do better (7176 x 1992: 925
+    // us and 937).
     constexpr int kEl = F32 ? 4 : 2;
+    const bool whole_lines = a.k * kEl % 128 == 0;
     constexpr int kRunBytes = TK / WK * kEl;   // bytes
     constexpr int kPitch = kRunBytes + 16;     // rows of 16 lanes start at different banks
-    constexpr int kLanes = kRunBytes / 16;     // lanes of a run
+    constexpr int kLanes = kRunBytes / 16;  // lanes of a run
+    constexpr int kRows = 64 / kLanes;      // runs of a store
+    constexpr int kStores = 16 / kRows;
     static_assert(16 * kPitch * T::kWaves <= T::kLds && 64 % kLanes == 0, "results fit LDS");
     char* const mine = lds + wave * (16 * kPitch);
 #pragma unroll
@@ -191,42 +200,41 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
             }
         }
         own_lds_done();
+        v4u v[kStores];
 #pragma unroll
-        for (int r0 = 0; r0 < 16; r0 += 64 / kLanes) {
-            const int r = r0 + lane / kLanes;
-            const int n = n0 + wn + j * 16 + r, k = k0 + wk + lane % kLanes * (16 / kEl);
-            const char* const from = mine + r * kPitch + lane % kLanes * 16;
-            if (n < a.n && k < a.k) {
-                const size_t at = ((size_t)e * a.n + n) * a.k + k;
-                if (F32) {
-                    v4f* o = reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at);
-                    const v4f v = *reinterpret_cast<const v4f*>(from);
-                    *o = ADD ? v + *o : v;
-                } else {
-                    *reinterpret_cast<v4u*>(reinterpret_cast<uint16_t*>(a.y) + at) = *reinterpret_cast<const v4u*>(from);
-                }
-            }
+        for (int r = 0; r < kStores; ++r)
+            v[r] = *reinterpret_cast<const v4u*>(mine + (r * kRows + lane / kLanes) * kPitch + lane % kLanes * 16);
+        const int k = k0 + wk + lane % kLanes * (16 / kEl);
+#pragma unroll
+        for (int r = 0; r < kStores; ++r) {
+            const int n = n0 + wn + j * 16 + r * kRows + lane / kLanes;
+            if (n >= a.n || k >= a.k) continue;
+            v4u* const o = reinterpret_cast<v4u*>(static_cast<char*>(a.y) + (((size_t)e * a.n + n) * a.k + k) * kEl);
+            if (ADD) v[r] = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, v[r]) + __builtin_bit_cast(v4f, *o));
+            if (whole_lines) __builtin_nontemporal_store(v[r], o);
+            asm volatile("");  // or the compiler makes one plain store of both
+            if (!whole_lines) *o = v[r];
         }
         own_lds_done();
     }
 }
 
-template <int TN, int TK, int WN, int WK, bool F32, bool ADD>
+template <int TN, int TK, int WN, int WK, int NS, bool F32, bool ADD>
 hipError_t launch_one(ExpertBf16Args a, hipStream_t stream) {
-    using T = WTile<TN, TK, WN, WK>;
+    using T = WTile<TN, TK, WN, WK, NS>;
     a.nt = (a.n + TN - 1) / TN;
     a.kt = (a.k + TK - 1) / TK;
     const long long blocks = ((long long)a.r.E * a.nt * a.kt + 255) / 256 * 256;  // whole runs of 32 on each XCD
     if (!grid_fits(blocks, T::kThreads)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((moedisp_expert_wgrad_bf16<TN, TK, WN, WK, F32, ADD>), dim3((unsigned)blocks),
+    hipLaunchKernelGGL((moedisp_expert_wgrad_bf16<TN, TK, WN, WK, NS, F32, ADD>), dim3((unsigned)blocks),
                        dim3(T::kThreads), T::kLds, stream, a);
     return hipGetLastError();
 }
 
 template <bool F32, bool ADD>
 hipError_t launch_tiles(const ExpertBf16Args& a, hipStream_t stream) {
-    if (expert_wgrad_bf16_tile(a.r.E, a.n, a.k).a == 256) return launch_one<256, 256, 4, 2, F32, ADD>(a, stream);
-    return launch_one<128, 128, 2, 2, F32, ADD>(a, stream);
+    if (expert_wgrad_bf16_tile(a.r.E, a.n, a.k).a == 256) return launch_one<256, 256, 4, 2, 4, F32, ADD>(a, stream);
+    return launch_one<128, 128, 2, 2, 3, F32, ADD>(a, stream);
 }
 
 }  // namespace

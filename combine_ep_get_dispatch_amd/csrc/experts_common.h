@@ -385,7 +385,7 @@ struct RouterShape {
 };
 RouterShape router_shape(int T, int E);
 TileShape expert_gemm_bf16_tile(int E, int n, int mean_rows);
-TileShape expert_gemm_w4_tile(int E, int n, int mean_rows);
+TileShape expert_gemm_w4_tile(int E, int n, int mean_rows, int w4_fmt);
 TileShape expert_wgrad_bf16_tile(int E, int n, int k);
 TileShape expert_wgrad_tile(int E, int n, int k, int scale_fmt, bool f32_out);
 long long swiglu_rows_at_once(int blocks);

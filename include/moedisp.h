@@ -530,9 +530,9 @@ typedef enum {
  *              scales of one group of channels lie together.
  *   y          [max_rows][n] bf16 or fp32 (out_dtype).
  * E2M1: a weight times its scale is taken as bf16 number, infinite beyond its
- * range (NaN times an x of 0).  INT4: sums over a group's x times code + 8 are binary32 and at most
- * 5 times as large as those of x times 8, so x has to stay below 2^122; a row
- * that holds an infinity gives NaN.  Rows, bounds, ws, overlap and alignment
+ * range (NaN times an x of 0).  INT4: a group's sums of x times the unsigned
+ * codes 0 .. 15, and of 8 x, are binary32, so that x has to stay below 2^116; a
+ * row that holds an infinity gives NaN.  Rows, bounds, ws, overlap and alignment
  * as said at moedisp_rows (UE8M0 scales: 4 bytes, bf16 scales: 4 bytes).
  * Equal inputs give equal bits.  Status bits: BAD_LAYOUT. */
 int ep_expert_gemm_w4(const moedisp_rows* rows, int32_t n, int32_t k, int32_t w4_fmt, const void* x, const void* w,
