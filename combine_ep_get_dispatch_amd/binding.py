@@ -65,7 +65,8 @@ EXPORTS = ("ep_workspace_bytes", "ep_workspace_init", "ep_get_dispatch_layout", 
            "ep_router_topk_backward")
 # tools (include/moedisp_tools.h): plan query and calibration probes, exported
 # by the same library
-CALIB_EXPORTS = ("ep_plan_query", "ep_expert_plan_query", "ep_balance_plan_query", "ep_probe_read", "ep_probe_copy", "ep_probe_fill")
+CALIB_EXPORTS = ("ep_plan_query", "ep_expert_plan_query", "ep_balance_plan_query", "ep_bf16_plan_query",
+                 "ep_router_plan_query", "ep_probe_read", "ep_probe_copy", "ep_probe_fill")
 
 
 class MoeDispError(RuntimeError):
@@ -137,6 +138,15 @@ class moedisp_expert_plan_info(C.Structure):
 class moedisp_balance_plan_info(C.Structure):
     _fields_ = [(n, C.c_int64) for n in ("struct_bytes", "tile_tokens", "tiles", "lanes", "rows_at_once", "passes",
                                          "backward_blocks")]
+
+
+class moedisp_bf16_plan_info(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("struct_bytes", "product_rows", "product_cols", "wgrad_cols",
+                                         "wgrad_channels", "e2m1_rows", "e2m1_cols", "int4_rows", "int4_cols")]
+
+
+class moedisp_router_plan_info(C.Structure):
+    _fields_ = [(n, C.c_int64) for n in ("struct_bytes", "lanes", "per_lane")]
 
 
 class moedisp_launch_info(C.Structure):
@@ -272,6 +282,10 @@ def load(path: str = LIB_PATH):
     L.ep_expert_plan_query.restype = C.c_int
     L.ep_balance_plan_query.argtypes = [Bl, C.POINTER(moedisp_balance_plan_info), sz]
     L.ep_balance_plan_query.restype = C.c_int
+    L.ep_bf16_plan_query.argtypes = [R, i32, i32, C.POINTER(moedisp_bf16_plan_info), sz]
+    L.ep_bf16_plan_query.restype = C.c_int
+    L.ep_router_plan_query.argtypes = [Rt, C.POINTER(moedisp_router_plan_info), sz]
+    L.ep_router_plan_query.restype = C.c_int
     L.ep_probe_read.argtypes = [P, C.c_size_t, P, P]
     L.ep_probe_read.restype = C.c_int
     L.ep_probe_copy.argtypes = [P, P, C.c_size_t, P]
@@ -961,6 +975,20 @@ def ep_balance_plan_query(balance) -> dict:
     """How the balance loss cuts its batch (no device touched)."""
     info = moedisp_balance_plan_info()
     _check("ep_balance_plan_query", load().ep_balance_plan_query(C.byref(balance), C.byref(info), C.sizeof(info)))
+    return _as_dict(info)
+
+
+def ep_bf16_plan_query(rows, n, k) -> dict:
+    """The tiles of the products of bf16 rows, as a dict."""
+    info = moedisp_bf16_plan_info()
+    _check("ep_bf16_plan_query", load().ep_bf16_plan_query(C.byref(rows), int(n), int(k), C.byref(info), C.sizeof(info)))
+    return _as_dict(info)
+
+
+def ep_router_plan_query(router) -> dict:
+    """How the router's choice lies in a wave, as a dict."""
+    info = moedisp_router_plan_info()
+    _check("ep_router_plan_query", load().ep_router_plan_query(C.byref(router), C.byref(info), C.sizeof(info)))
     return _as_dict(info)
 
 

@@ -464,6 +464,41 @@ int ep_expert_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, int32_t
     return MOEDISP_OK;
 }
 
+int ep_bf16_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, moedisp_bf16_plan_info* info,
+                       size_t info_bytes) {
+    if (!info || info_bytes != sizeof(moedisp_bf16_plan_info)) return MOEDISP_ERR_INVALID_ARG;
+    memset(info, 0, sizeof *info);
+    static const int32_t some_bounds = 0;  // the query has no bounds; the rows' own rules are checked
+    int st = check_rows(rows, &some_bounds);
+    if (st || (st = check_bf16_product(n, k, 8, 8, MOEDISP_BF16))) return st;
+    info->struct_bytes = (int64_t)sizeof *info;
+    const int E = rows->num_experts, mean = mean_rows(*rows);
+    const TileShape g = expert_gemm_bf16_tile(E, n, mean), w = expert_wgrad_bf16_tile(E, n, k);
+    const TileShape e = expert_gemm_w4_tile(E, n, mean, MOEDISP_W4_E2M1);
+    const TileShape i = expert_gemm_w4_tile(E, n, mean, MOEDISP_W4_INT4);
+    info->product_rows = g.a;
+    info->product_cols = g.b;
+    info->wgrad_cols = w.a;
+    info->wgrad_channels = w.b;
+    info->e2m1_rows = e.a;
+    info->e2m1_cols = e.b;
+    info->int4_rows = i.a;
+    info->int4_cols = i.b;
+    return MOEDISP_OK;
+}
+
+int ep_router_plan_query(const moedisp_router* r, moedisp_router_plan_info* info, size_t info_bytes) {
+    if (!info || info_bytes != sizeof(moedisp_router_plan_info)) return MOEDISP_ERR_INVALID_ARG;
+    memset(info, 0, sizeof *info);
+    const int st = check_router(r);
+    if (st) return st;
+    info->struct_bytes = (int64_t)sizeof *info;
+    const RouterShape s = router_shape(r->num_tokens, r->num_experts);
+    info->lanes = s.lanes;
+    info->per_lane = s.per_lane;
+    return MOEDISP_OK;
+}
+
 int ep_balance_plan_query(const moedisp_balance* b, moedisp_balance_plan_info* info, size_t info_bytes) {
     if (!info || info_bytes != sizeof(moedisp_balance_plan_info)) return MOEDISP_ERR_INVALID_ARG;
     memset(info, 0, sizeof *info);

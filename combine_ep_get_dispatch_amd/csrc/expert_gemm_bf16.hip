@@ -279,19 +279,20 @@ hipError_t launch_variant(const ExpertBf16Args& a, int mean_rows, hipStream_t st
 
 }  // namespace
 
+// Times of a round of all compute units for 4096 channels, whose weights other
+// workgroups read as well.  Experts, usual rows, K, n, us (NK):
+//                              32x128  64x256  96x256  128x256  160x256  256x256
+//       8,   16, 4096, 8192       110     121     122      121      123      130
+//       8,   64, 4096, 8192       146     142     129      130      132      140
+//      64,   62, 2048, 4096       279     229     198      199      204      249
+//     256,  128, 7168, 4096      5934    3972    3529     3872     2882     3467
+//      16,  250, 2048, 2000        69      60      52       57       41       48
+//      30,  400, 1024, 2048       119      82      74       71       67       64
+//       8, 4096, 4096, 8192      5580    3030    2389     2074     2008     1728
 TileShape expert_gemm_bf16_tile(int E, int n, int mean_rows) {
-    const long long small = (long long)E * (((long long)mean_rows + 31) / 32) * ((n + 127) / 128);
-    if (mean_rows <= 16 || small <= 2 * kCus || (mean_rows <= 32 && small <= 4 * kCus)) return {32, 128};
-    if (mean_rows <= 32 || small <= 4 * kCus) return {64, 256};
-    if (mean_rows <= 72) return {96, 256};
-    if (mean_rows <= 112) return {128, 256};
-    if (mean_rows <= 144) return {160, 256};
-    const long long nt = (n + 255) / 256;
-    const long long large = E * (((long long)mean_rows + 255) / 256) * nt;
-    const long long half = E * (((long long)mean_rows + 127) / 128) * nt;
-    const long long rounds = (large + kCus - 1) / kCus * kCus;
-    if (rounds * 4 > half * 3) return {128, 256};
-    return {256, 256};
+    static const TileTime kinds[] = {{32, 128, 2, 44}, {64, 256, 1, 47},  {96, 256, 1, 56},
+                                     {128, 256, 1, 65}, {160, 256, 1, 78}, {256, 256, 1, 112}};
+    return tile_by_rounds(kinds, 6, E, n, mean_rows);
 }
 
 hipError_t launch_expert_gemm_bf16(const ExpertBf16Args& a, int mean_rows, bool kn, bool f32_out,

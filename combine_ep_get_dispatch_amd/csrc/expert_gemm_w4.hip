@@ -18,8 +18,6 @@
 // its channels are 32 (lane / 16) + 8 d .. + 7, and the rows' operands are read
 // to match.  A lane's 32 channels are one group of E2M1 weights, the four
 // lanes' 128 one of the integers.
-#include <math.h>
-
 #include "experts_common.h"
 
 namespace moedisp {
@@ -315,15 +313,8 @@ hipError_t launch_variant(const ExpertW4Args& a, int mean_rows, hipStream_t stre
 
 }  // namespace
 
-// The tile whose rounds take the least time.  Experts' rows are taken to
-// scatter round the usual number as random choices do, by its square root.  A
-// round of all compute units takes, for 4096 channels (us; 16 x 128, 32 x 256
-// and 64 x 128 have two workgroups to a unit and go on into the next round, the
-// others start together):
-//              16x128  32x256  64x128  96x256  160x256
-//     E2M1         22      48      38      48       69
-//     integers     24      56      52      63       90
-// 8 experts, K = 4096, integers, us for usual rows (columns):
+// Times of a round of all compute units for 4096 channels.  8 experts, K =
+// 4096, integers, us for usual rows (columns):
 //     rows (n)    16x128  32x256  64x128  96x256  160x256
 //       16 (8192)     39      38      52      62       87
 //       32 (8192)     53      53      52      62       87
@@ -332,31 +323,11 @@ hipError_t launch_variant(const ExpertW4Args& a, int mean_rows, hipStream_t stre
 //      125 (8208)    190     117     117     175      171
 //     1024 (8192)   1343     804     802     709      607
 TileShape expert_gemm_w4_tile(int E, int n, int mean_rows, int w4_fmt) {
-    struct Kind {
-        int rows, cols, at_once;
-        double us[2];
-    };
-    static const Kind kinds[] = {{16, 128, 2 * kCus, {22, 24}}, {32, 256, 2 * kCus, {48, 56}},
-                                 {64, 128, 2 * kCus, {38, 52}}, {96, 256, kCus, {48, 63}},
-                                 {160, 256, kCus, {69, 90}}};
-    const double mean = mean_rows, spread = 2.0 * sqrt(mean);
-    TileShape best = {16, 128};
-    double least = 0.0;
-    for (const Kind& k : kinds) {
-        // row tiles of an expert: one more for each multiple of the tile that is exceeded
-        const double whole = floor(fmax(mean - spread, 0.0) / k.rows);
-        double row_tiles = 1.0 + whole;
-        for (double m = whole + 1.0; m * k.rows < mean + spread; m += 1.0)
-            row_tiles += fmin(1.0, fmax(0.0, (mean - m * k.rows) / spread + 0.5));
-        double rounds = row_tiles * E * ((n + k.cols - 1) / k.cols) / k.at_once;
-        rounds = k.at_once > kCus ? fmax(rounds, 1.0) : ceil(rounds);
-        const double us = rounds * k.us[w4_fmt == MOEDISP_W4_INT4];
-        if (k.rows == 16 || us < least) {
-            best = {k.rows, k.cols};
-            least = us;
-        }
-    }
-    return best;
+    static const TileTime e2m1[] = {{16, 128, 2, 22}, {32, 256, 2, 48}, {64, 128, 2, 38}, {96, 256, 1, 48},
+                                    {160, 256, 1, 69}};
+    static const TileTime int4[] = {{16, 128, 2, 24}, {32, 256, 2, 56}, {64, 128, 2, 52}, {96, 256, 1, 63},
+                                    {160, 256, 1, 90}};
+    return tile_by_rounds(w4_fmt == MOEDISP_W4_INT4 ? int4 : e2m1, 5, E, n, mean_rows);
 }
 
 hipError_t launch_expert_gemm_w4(const ExpertW4Args& a, int mean_rows, int w4_fmt, bool f32_out, hipStream_t stream) {

@@ -3,6 +3,8 @@
 // combine.
 #pragma once
 
+#include <math.h>
+
 #include "kernels_common.h"
 
 namespace moedisp {
@@ -378,6 +380,36 @@ inline int balance_lanes(int E) {
 struct TileShape {
     int a, b;
 };
+// A tile and the time of a round of its workgroups on all compute units, so
+// many to a unit (any unit of time).
+struct TileTime {
+    int rows, cols, per_cu;
+    double time;
+};
+// The tile whose rounds take the least time, the first of equal ones.
+// Experts' rows are taken to scatter round the usual number as random choices
+// do, by its square root.  Workgroups that share a unit go on into the next
+// round; those alone there start together.
+inline TileShape tile_by_rounds(const TileTime* kinds, int count, int E, int n, int mean_rows) {
+    const double mean = mean_rows, spread = 2.0 * sqrt(mean);
+    TileShape best = {kinds[0].rows, kinds[0].cols};
+    double least = 0.0;
+    for (int i = 0; i < count; ++i) {
+        const TileTime& k = kinds[i];
+        // row tiles of an expert: one more for each multiple of the tile that is exceeded
+        const double whole = floor(fmax(mean - spread, 0.0) / k.rows);
+        double row_tiles = 1.0 + whole;
+        for (double m = whole + 1.0; m * k.rows < mean + spread; m += 1.0)
+            row_tiles += fmin(1.0, fmax(0.0, (mean - m * k.rows) / spread + 0.5));
+        double rounds = row_tiles * E * (((long long)n + k.cols - 1) / k.cols) / (k.per_cu * kCus);
+        rounds = k.per_cu > 1 ? fmax(rounds, 1.0) : ceil(rounds);
+        if (i == 0 || rounds * k.time < least) {
+            best = {k.rows, k.cols};
+            least = rounds * k.time;
+        }
+    }
+    return best;
+}
 TileShape expert_gemm_tile(int E, int n, int mean_rows, bool f32_out);
 // How the router's choice lies in a wave: lanes of a row, experts of a lane.
 struct RouterShape {

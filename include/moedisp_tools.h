@@ -136,6 +136,30 @@ typedef struct moedisp_expert_plan_info {
 int ep_expert_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, int32_t scale_fmt, int32_t out_dtype,
                          moedisp_expert_plan_info* info, size_t info_bytes);
 
+/* Tiles of the products of bf16 rows for one set of rows. */
+typedef struct moedisp_bf16_plan_info {
+    int64_t struct_bytes;                     /* sizeof(moedisp_bf16_plan_info) */
+    int64_t product_rows, product_cols;       /* ep_expert_gemm_bf16: rows by columns of y */
+    int64_t wgrad_cols, wgrad_channels;       /* ep_expert_wgrad_bf16: columns of dy by channels of x */
+    int64_t e2m1_rows, e2m1_cols;             /* ep_expert_gemm_w4, MOEDISP_W4_E2M1 */
+    int64_t int4_rows, int4_cols;             /* ep_expert_gemm_w4, MOEDISP_W4_INT4 */
+} moedisp_bf16_plan_info;
+
+/* As ep_expert_plan_query, for calls of n columns and k channels, multiples of
+ * 8 (tiles of the 4-bit products are what those calls would take if their own
+ * rules for n and k held). */
+int ep_bf16_plan_query(const moedisp_rows* rows, int32_t n, int32_t k, moedisp_bf16_plan_info* info,
+                       size_t info_bytes);
+
+/* How ep_router_topk and its backward pass lie in a wave. */
+typedef struct moedisp_router_plan_info {
+    int64_t struct_bytes;      /* sizeof(moedisp_router_plan_info) */
+    int64_t lanes, per_lane;   /* lanes of a token, experts of a lane */
+} moedisp_router_plan_info;
+
+/* As ep_expert_plan_query, for the shape of a router. */
+int ep_router_plan_query(const moedisp_router* r, moedisp_router_plan_info* info, size_t info_bytes);
+
 /* How ep_balance_loss and its backward pass cut a batch. */
 typedef struct moedisp_balance_plan_info {
     int64_t struct_bytes;                /* sizeof(moedisp_balance_plan_info) */

@@ -32,6 +32,14 @@ def weights4(w, sc, fmt):
     return unpack4(w, fmt) * scales4(sc, fmt)
 
 
+def hint_for(E, N, K, field, tile):
+    """expected_rows for which the plan takes this tile."""
+    for rows in [*range(1, 64), *range(64, 2000, 5)]:
+        if M.ep_bf16_plan_query(M.moedisp_rows.contiguous(E, 4096, rows), N, K)[field] == tile:
+            return rows
+    raise AssertionError(f"no hint takes {field} {tile}")
+
+
 class Bf16Problem:
     """Rows, weights and bounds of one product on the GPU.  Every byte of the
     row buffers that no expert owns holds NaN, so that reading it shows."""

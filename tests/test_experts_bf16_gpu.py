@@ -10,7 +10,7 @@ import torch
 
 import combine_ep_get_dispatch_amd as M
 from combine_ep_get_dispatch_amd import binding as B
-from bf16_reference import Bf16Problem
+from bf16_reference import Bf16Problem, hint_for
 from experts_reference import swiglu64
 from test_experts_gpu import COUNTS, within
 
@@ -55,10 +55,11 @@ def test_product_sizes(N, K, layout, out):
 @pytest.mark.parametrize("out", OUTS)
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("K", [56, 64, 128, 200, 1096])
-@pytest.mark.parametrize("expected", [8, 40, 100, 1000])
-def test_product_every_tile(expected, K, layout, out):
+@pytest.mark.parametrize("tile", [32, 64, 96, 128, 160, 256])
+def test_product_every_tile(tile, K, layout, out):
     counts = [300, 0, 31, 513, 1, 256] * 3
-    check_gemm(Bf16Problem(counts, 1288, K, seed=K, expected=expected), layout, out, f"{expected} {K}")
+    hint = hint_for(len(counts), 1288, K, "product_rows", tile)
+    check_gemm(Bf16Problem(counts, 1288, K, seed=K, expected=hint), layout, out, f"{tile} {K}")
 
 
 @pytest.mark.parametrize("out", OUTS)

@@ -12,7 +12,7 @@ import torch
 
 import combine_ep_get_dispatch_amd as M
 from combine_ep_get_dispatch_amd import binding as B
-from bf16_reference import Bf16Problem, scales4, unpack4, weights4
+from bf16_reference import Bf16Problem, hint_for, scales4, unpack4, weights4
 from test_experts_gpu import COUNTS, within
 
 pytestmark = pytest.mark.gpu
@@ -84,10 +84,12 @@ def test_sizes(N, K, fmt, out):
 @pytest.mark.parametrize("out", OUTS)
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("K", [128, 256, 640, 1152])
-@pytest.mark.parametrize("expected", [1, 16, 40, 1000])
-def test_every_tile(expected, K, fmt, out):
+@pytest.mark.parametrize("tile", [16, 32, 64, 96, 160])
+def test_every_tile(tile, K, fmt, out):
     counts = [300, 0, 31, 513, 1, 256] * 3
-    check(Bf16Problem(counts, 1296, K, seed=K, expected=expected), fmt, out, f"{expected} {K}")
+    N = 4112 if tile == 32 else 1296
+    hint = hint_for(len(counts), N, K, "int4_rows" if fmt == M.W4_INT4 else "e2m1_rows", tile)
+    check(Bf16Problem(counts, N, K, seed=K, expected=hint), fmt, out, f"{tile} {K}")
 
 
 @pytest.mark.parametrize("out", OUTS)
