@@ -23,7 +23,7 @@ constexpr int kSeqThreads = 1024;
 constexpr int kSeqCols = 64;  // experts of a workgroup that sums tiles
 
 template <int LPR>
-__device__ inline int lanes_sum(int v) {
+__device__ inline int lanes_count(int v) {
     return __float_as_int(row_reduce<LPR>(__int_as_float(v), [](float x, float y) {
         return __int_as_float(__float_as_int(x) + __float_as_int(y));
     }));
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(kBalThreads) void moedisp_balance_backward(BalanceA
             c[v] = e < a.E ? a.tokens_per_expert[(size_t)seq * a.E + e] : 0;
             slots += c[v];
         }
-        const int mean = lanes_sum<LPR>(slots) / a.E;
+        const int mean = lanes_count<LPR>(slots) / a.E;
         float w[N];
 #pragma unroll
         for (int v = 0; v < N; ++v)
