@@ -329,6 +329,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _Args:
     """Checks of the tensor arguments of one call, before any pointer crosses
     the C ABI: each tensor must have an accepted element type, be contiguous
@@ -337,6 +340,8 @@ class _Args:
     test sees each size and type check).  A failed check raises MoeDispError
     (invalid argument): no kernel is ever handed a buffer smaller than the
     shape says, or an int64 table read as int32."""
+
+    __slots__ = ("call", "tensors", "read", "out")
 
     def __init__(self, call: str):
         self.call = call
@@ -370,13 +375,20 @@ class _Args:
     def arg(self, name: str, t, dtypes, nbytes: int, optional: bool = False, written: bool = False):
         """As need(); returns the tensor's address (None for none).  The call
         writes to a tensor that is `written`."""
-        if type(t) is not torch.Tensor or (dtypes is not None and t.dtype not in dtypes) or not t.is_contiguous() \
-                or t.nbytes < nbytes:
+        if type(t) is torch.Tensor and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
+            have = t.nbytes
+            if have < nbytes:
+                self.need(name, t, dtypes, nbytes, optional)  # says so
+        else:
             self.need(name, t, dtypes, nbytes, optional)  # takes a subclass or none, else says what is wrong
             if t is None:
                 return None
+            have = t.nbytes
         at = t.data_ptr()
-        (self.out if written else self.read).append((at, at + t.nbytes, name, t))
+        if written:
+            self.out.append((at, at + have, name, t))
+        else:
+            self.read.append((at, at + have, name, t))
         return at
 
     def on_device(self, stream):
@@ -385,20 +397,23 @@ class _Args:
         memory with any other.  Returns the GPU's index and the stream's
         handle (its current stream unless one is given), so that the call does
         not depend on which device is current."""
-        every = self.read + self.out
-        dev = every[0][3].get_device()
+        read, out = self.read, self.out
+        dev = (read or out)[0][3].get_device()
         same = dev >= 0
-        for a in every:
-            if a[3].get_device() != dev:
+        for _, _, _, t in read:
+            if t.get_device() != dev:
                 same = False
-        left = len(self.read)
-        for at, end, name, _ in self.out:
-            left += 1
-            for oat, oend, other, _ in self.read + self.out[left - len(self.read):]:
+        for i, (at, end, name, t) in enumerate(out):
+            if t.get_device() != dev:
+                same = False
+            for oat, oend, other, _ in read:
+                if at < oend and oat < end:
+                    self.fail(f"{name} overlaps {other}")
+            for oat, oend, other, _ in out[i + 1:]:
                 if at < oend and oat < end:
                     self.fail(f"{name} overlaps {other}")
         if not same:
-            self.tensors = [(n, t, t.nbytes) for _, _, n, t in every]
+            self.tensors = [(n, t, t.nbytes) for _, _, n, t in read + out]
             self.done()
             self.fail("the tensors lie on different GPUs: " + ", ".join(f"{n} on {t.device}" for n, t, _ in self.tensors))
         if stream is None:
@@ -775,7 +790,7 @@ def _scales(A, name, t, fmt, count, optional=False, written=False):
 def _on(dev: int, call: str, *args):
     """The C call with `dev` as the current device."""
     f = getattr(_lib or load(), call)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = f(*args)
     else:
         with torch.cuda.device(dev):

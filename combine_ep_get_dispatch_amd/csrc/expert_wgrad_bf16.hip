@@ -211,9 +211,7 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
             if (n >= a.n || k >= a.k) continue;
             v4u* const o = reinterpret_cast<v4u*>(static_cast<char*>(a.y) + (((size_t)e * a.n + n) * a.k + k) * kEl);
             if (ADD) v[r] = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, v[r]) + __builtin_bit_cast(v4f, *o));
-            if (whole_lines) __builtin_nontemporal_store(v[r], o);
-            asm volatile("");  // or the compiler makes one plain store of both
-            if (!whole_lines) *o = v[r];
+            store16(o, v[r], whole_lines);
         }
         own_lds_done();
     }
