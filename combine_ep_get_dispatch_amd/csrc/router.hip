@@ -27,6 +27,13 @@
 //     normalised            dz = s (g - sum_i g_i s_i), sigmoid: times 1 - score
 //     softmax               dz = p ([chosen] g - sum_i g_i p_i), all experts
 //     sigmoid               dz = g s (1 - s)
+//
+// What bounds it.  131072 rows of 256 bf16 logits, top-8: 37 us forward (75 MB,
+// 2 TB/s), instructions: about a third each for the sort, the k rounds, and the
+// exponentials with the keys; 31 us backward (142 MB, 4.6 TB/s).  128 rows
+// with bias and groups: 6.7 us, latency of dependent lane exchanges (13 with 16
+// lanes a row).  The compiler's accesses by index for lists that move up took
+// 343 us forward, binary64 keys for bf16 logits 44.
 #include <type_traits>
 
 #include "experts_common.h"
@@ -625,6 +632,9 @@ hipError_t launch(const RouterArgs& a, bool backward, hipStream_t stream) {
 
 }  // namespace
 
+// 16 lanes a row let a wave work on four; a whole wave is quicker where there
+// are few rows (256 experts, 128 rows with bias and groups: 8.7 us a call and 13;
+// 131072 rows: 126 us both directions and 69).
 RouterShape router_shape(int T, int E) {
     if (E <= 64) return {16, 4};
     if (E <= 128) return {16, 8};

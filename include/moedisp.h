@@ -391,9 +391,9 @@ int ep_combine_padded(const moedisp_shape* shape, int32_t expert_stride, const v
  * accumulate reads the dw it writes).  Calls of different workspaces share
  * nothing and may run at once.
  * Every entry needs 16-byte aligned row and weight buffers of whole 16-byte
- * rows, 4-byte aligned binary32 scales, and takes OCP E4M3 codes with one
- * scale per block of 128 channels in the format scale_fmt
- * (moedisp_scale_fmt), as dispatch leaves them. */
+ * rows and 4-byte aligned binary32 scales.  Those with a scale_fmt
+ * (moedisp_scale_fmt) take OCP E4M3 codes with one scale per block of 128
+ * channels, as the quantising dispatch leaves them; the others take bf16 rows. */
 typedef struct {
     int32_t num_experts;      /* E in [1, 4096] */
     int32_t max_rows;         /* rows of the row buffers, in [0, 2^30) */
@@ -583,7 +583,7 @@ int ep_router_topk(const moedisp_router* r, const void* logits, const float* bia
  *   d_topk_weights  fp32 [T][k].
  *   d_logits        [T][E] in the type of the logits, all written.
  * An expert that a token names twice gets the sum of both slots, each with its
- * own weight.  Status bits: BAD_EXPERT_ID (that slot has no gradient). */
+ * own weight (of more than two, in no fixed order).  Status bits: BAD_EXPERT_ID (that slot has no gradient). */
 int ep_router_topk_backward(const moedisp_router* r, const void* logits, const int32_t* topk_idx,
                             const float* d_topk_weights, void* d_logits, void* ws, size_t ws_bytes, void* stream);
 
