@@ -332,7 +332,44 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class _Args:
+class _PyChecks:
+    """_checks.Checks (csrc/checks.cpp) in Python."""
+    __slots__ = ("call", "tensors", "read", "out")
+
+    def __init__(self, call: str):
+        self.call = call
+        self.tensors, self.read, self.out = [], [], []  # by need(); by arg(): read, written
+
+    def arg(self, name: str, t, dtypes, nbytes: int, optional: bool = False, written: bool = False):
+        """As need(); returns the tensor's address (None for none).  The call
+        writes to a tensor that is `written`."""
+        if type(t) is not torch.Tensor or (dtypes is not None and t.dtype not in dtypes) or not t.is_contiguous() \
+                or t.nbytes < nbytes:
+            self.need(name, t, dtypes, nbytes, optional)  # takes a subclass or none, else says what is wrong
+            if t is None:
+                return None
+        at = t.data_ptr()
+        (self.out if written else self.read).append((at, at + t.nbytes, name, t))
+        return at
+
+    def on_device(self, stream):
+        """As done(), for arguments taken by arg(); every tensor must lie on
+        one GPU, the stream's if one is given, and those written must share no
+        memory with any other.  Returns the GPU's index and the stream's
+        handle (its current stream unless one is given), so that the call does
+        not depend on which device is current."""
+        return self.resolve(self.read, self.out, stream)
+
+
+try:
+    from . import _checks
+    _checks.use_stream_of(_raw_stream)
+    _Checks = _checks.Checks
+except ImportError:  # not built, or for another torch
+    _Checks = _PyChecks
+
+
+class _Args(_Checks):
     """Checks of the tensor arguments of one call, before any pointer crosses
     the C ABI: each tensor must have an accepted element type, be contiguous
     and hold at least the bytes the shape needs (need), and every tensor must
@@ -340,12 +377,7 @@ class _Args:
     test sees each size and type check).  A failed check raises MoeDispError
     (invalid argument): no kernel is ever handed a buffer smaller than the
     shape says, or an int64 table read as int32."""
-
-    __slots__ = ("call", "tensors", "read", "out")
-
-    def __init__(self, call: str):
-        self.call = call
-        self.tensors, self.read, self.out = [], [], []  # by need(); by arg(): read, written
+    __slots__ = ()
 
     def fail(self, msg: str):
         raise MoeDispError(self.call, ERR_INVALID_ARG, msg)
@@ -372,44 +404,16 @@ class _Args:
             if t.device.type != "cuda":
                 self.fail(f"{name} is on {t.device}, expected a GPU tensor")
 
-    def arg(self, name: str, t, dtypes, nbytes: int, optional: bool = False, written: bool = False):
-        """As need(); returns the tensor's address (None for none).  The call
-        writes to a tensor that is `written`."""
-        if type(t) is torch.Tensor and (dtypes is None or t.dtype in dtypes) and t.is_contiguous():
-            have = t.nbytes
-            if have < nbytes:
-                self.need(name, t, dtypes, nbytes, optional)  # says so
-        else:
-            self.need(name, t, dtypes, nbytes, optional)  # takes a subclass or none, else says what is wrong
-            if t is None:
-                return None
-            have = t.nbytes
-        at = t.data_ptr()
-        if written:
-            self.out.append((at, at + have, name, t))
-        else:
-            self.read.append((at, at + have, name, t))
-        return at
-
-    def on_device(self, stream):
-        """As done(), for arguments taken by arg(); every tensor must lie on
-        one GPU, the stream's if one is given, and those written must share no
-        memory with any other.  Returns the GPU's index and the stream's
-        handle (its current stream unless one is given), so that the call does
-        not depend on which device is current."""
-        read, out = self.read, self.out
+    def resolve(self, read, out, stream):
+        """on_device() of arguments (address, end, name, tensor) that are read
+        or written; says what is wrong."""
         dev = (read or out)[0][3].get_device()
         same = dev >= 0
-        for _, _, _, t in read:
+        for _, _, _, t in read + out:
             if t.get_device() != dev:
                 same = False
-        for i, (at, end, name, t) in enumerate(out):
-            if t.get_device() != dev:
-                same = False
-            for oat, oend, other, _ in read:
-                if at < oend and oat < end:
-                    self.fail(f"{name} overlaps {other}")
-            for oat, oend, other, _ in out[i + 1:]:
+        for i, (at, end, name, _) in enumerate(out):
+            for oat, oend, other, _ in read + out[i + 1:]:
                 if at < oend and oat < end:
                     self.fail(f"{name} overlaps {other}")
         if not same:

@@ -1,8 +1,10 @@
-"""Build libmoedisp.so (gfx950) from csrc/ with hipcc, in-tree."""
+"""Build libmoedisp.so (gfx950) from csrc/ with hipcc, in-tree, and the Python
+binding's argument checks (_checks.so) with the host compiler."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -37,5 +39,27 @@ def build(out: str = LIB, extra_flags=(), verbose: bool = False) -> str:
     return out
 
 
+CHECKS = os.path.join(HERE, "_checks.so")
+
+
+def build_checks(out: str = CHECKS, verbose: bool = False) -> str:
+    """The binding works without it, more slowly."""
+    import torch
+    from torch.utils import cpp_extension
+    inc = [f"-I{p}" for p in [sysconfig.get_paths()["include"], *cpp_extension.include_paths()]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = out + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *inc, "-o", tmp,
+           os.path.join(CSRC, "checks.cpp"), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     print(build(verbose=True))
+    print(build_checks(verbose=True))
