@@ -775,6 +775,7 @@ def ep_combine_padded(shape, expert_stride, expert_out, recv_src_idx, recv_weigh
 
 
 _U8 = (torch.uint8,)
+_FLAGS = (torch.uint8, torch.bool)
 _BF16 = (torch.bfloat16,)
 
 
@@ -916,7 +917,7 @@ def _choice(A, r, logits):
 def ep_router_topk(router, logits, bias, live, topk_idx, topk_weights, stream=None):
     A = _Args("ep_router_topk")
     T, E, k, _, _, z = _choice(A, router, logits)
-    args = (z, A.arg("bias", bias, _F32, 4 * E, optional=True), A.arg("live", live, _U8, T, optional=True),
+    args = (z, A.arg("bias", bias, _F32, 4 * E, optional=True), A.arg("live", live, _FLAGS, T, optional=True),
             A.arg("topk_idx", topk_idx, _INT32, 4 * T * k, written=True),
             A.arg("topk_weights", topk_weights, _F32, 4 * T * k, written=True))
     dev, st = A.on_device(stream)

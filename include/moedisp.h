@@ -573,7 +573,7 @@ typedef struct {
  *   logits        [T][E] bf16 or fp32, 16-byte aligned.
  *   bias          fp32 [E] or NULL; takes part in the choice only.
  *   live          uint8 [T] or NULL: 0 for tokens that are padding, all of
- *                 whose slots are -1.
+ *                 whose slots are -1 (else not 0).
  *   topk_idx      int32 [T][k];  topk_weights fp32 [T][k]. */
 int ep_router_topk(const moedisp_router* r, const void* logits, const float* bias, const uint8_t* live,
                    int32_t* topk_idx, float* topk_weights, void* stream);

@@ -1,17 +1,20 @@
 """The binding's argument checks in C++ and in Python say the same (no GPU
 needed for what is refused; with one, that both find the same addresses,
 GPU and stream)."""
+import os
 import sys
 
 import pytest
 import torch
 
 from combine_ep_get_dispatch_amd import binding as B
+from combine_ep_get_dispatch_amd.build import CHECKS
 
 PyArgs = type("PyArgs", (B._PyChecks,), {n: B._Args.__dict__[n] for n in ("fail", "need", "done", "resolve")})
 BOTH = [B._Args, PyArgs]
 
 
+@pytest.mark.skipif(not os.path.exists(CHECKS), reason="_checks.so is not built; the checks run in Python")
 def test_the_native_checks_are_in_use():
     from combine_ep_get_dispatch_amd import _checks
     assert issubclass(B._Args, _checks.Checks)

@@ -139,7 +139,7 @@ def test_rows_without_experts(score, dt):
     z[7, 5] = float("nan")
     live = torch.ones(40, dtype=torch.uint8)
     live[8] = live[39] = 0
-    live = live.cuda()
+    live = live.cuda() if score == M.SCORE_SOFTMAX else live.bool().cuda()
     z[39] = float("nan")
     for bias in (None, torch.linspace(-1, 1, 20).cuda()):
         for kw in ({}, dict(groups=5, topk_groups=2), dict(normalise=False)):
