@@ -177,10 +177,7 @@ __device__ inline float lanes_max(float v) {
     return row_reduce<LPR>(v, [](float x, float y) { return fmaxf(x, y); });
 }
 
-// Results beyond what the L2s hold together are not kept there for the next
-// kernel: they leave at once, which saves room and time (32768 rows of 2048 in
-// bf16 from 4096: 64 us instead of 80).
-constexpr long long kL2Bytes = 32ll << 20;
+constexpr long long kCacheBytes = 256ll << 20;  // of the memory-side cache
 
 // 16 bytes, past the caches if so.
 __device__ inline void store16(void* to, v4u v, bool past) {
@@ -339,7 +336,6 @@ struct SwigluArgs {
     const uint16_t* dh;   // backward
     uint16_t* dgu;        // backward: bf16 gradient, may be null
     uint16_t* h;          // forward in bf16
-    bool past;            // h goes past the caches
     uint8_t* q;           // codes of h, or of the gradient (may be null)
     void* q_scales;
     WsHeader* hdr;
@@ -447,7 +443,7 @@ hipError_t launch_expert_gemm_bf16(const ExpertBf16Args& a, int mean_rows, bool 
                                    hipStream_t stream);
 hipError_t launch_expert_gemm_w4(const ExpertW4Args& a, int mean_rows, int w4_fmt, bool f32_out, hipStream_t stream);
 hipError_t launch_expert_wgrad_bf16(const ExpertBf16Args& a, bool f32_out, bool accumulate, hipStream_t stream);
-hipError_t launch_swiglu_bf16(SwigluArgs a, hipStream_t stream);
+hipError_t launch_swiglu_bf16(const SwigluArgs& a, hipStream_t stream);
 hipError_t launch_swiglu(const SwigluArgs& a, int scale_fmt, hipStream_t stream);
 hipError_t launch_swiglu_backward(const SwigluArgs& a, int scale_fmt, hipStream_t stream);
 hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t stream);
