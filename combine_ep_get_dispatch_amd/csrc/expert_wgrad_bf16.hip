@@ -6,8 +6,8 @@
 // What bounds it.  Many rows (32768 over 8 experts, 4096 x 4096): 0.87 ms, 1.26
 // PFLOP/s, products with the transposing reads beside them (matrix units 0.6 of
 // the time).  Few rows (7782 over 64, 7168 x 2048, fp32): the writes, 3.8 GB in
-// 0.69 ms, 5.5 TB/s; where rows start inside a line (7176 x 1992) 0.92 ms.  An
-// expert's rows are not split.
+// 0.86 ms, 4.4 TB/s (7176 x 1992, tiles cut at both edges: 0.92 ms).  An expert's
+// rows are not split.
 //
 // How.  A workgroup computes one tile over all rows of its expert, 32 rows a
 // step, two or three steps of loads under way.  Both operands are contracted over
@@ -178,13 +178,9 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
     }
 
     // Results by way of LDS, a wave's 16 columns at a time in a place of its
-    // own, so that rows of dw are written in runs of a wave's channels.  Runs of
-    // whole lines of 128 bytes leave the caches at once (64 experts of 7168 x
-    // 2048, fp32: 693 us, 862 with plain stores); rows that start inside a line
-    // have runs that meet there, where plain stores do better (7176 x 1992: 925
-    // us and 937).
+    // own, so that rows of dw are written in runs of a wave's channels (64 experts
+    // of 7176 x 1992, fp32: 984 -> 927 us).
     constexpr int kEl = F32 ? 4 : 2;
-    const bool whole_lines = a.k * kEl % 128 == 0;
     constexpr int kRunBytes = TK / WK * kEl;   // bytes
     constexpr int kPitch = kRunBytes + 16;     // rows of 16 lanes start at different banks
     constexpr int kLanes = kRunBytes / 16;  // lanes of a run
@@ -217,7 +213,7 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
             if (n >= a.n || k >= a.k) continue;
             v4u* const o = reinterpret_cast<v4u*>(static_cast<char*>(a.y) + (((size_t)e * a.n + n) * a.k + k) * kEl);
             if (ADD) v[r] = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, v[r]) + __builtin_bit_cast(v4f, *o));
-            store16(o, v[r], whole_lines);
+            *o = v[r];
         }
         own_lds_done();
     }
@@ -245,7 +241,7 @@ hipError_t launch_tiles(const ExpertBf16Args& a, hipStream_t stream) {
 
 // Tiles of 256 x 256 move the fewest bytes per product (8 experts of 4096 x
 // 4096 and 4096 rows each: 869 us against 1054 with 128 x 128; 64 of 7168 x
-// 2048 and 122 rows, fp32: 690 against 975 before whole lines).  Tiles of 128 x
+// 2048 and 122 rows, fp32: 858 against 975).  Tiles of 128 x
 // 128, three workgroups to a unit, where large ones, in whole rounds of one for
 // each unit, cover a fifth more than small ones do.
 TileShape expert_wgrad_bf16_tile(int E, int n, int k) {

@@ -179,13 +179,6 @@ __device__ inline float lanes_max(float v) {
 
 constexpr long long kCacheBytes = 256ll << 20;  // of the memory-side cache
 
-// 16 bytes, past the caches if so.
-__device__ inline void store16(void* to, v4u v, bool past) {
-    if (past) __builtin_nontemporal_store(v, static_cast<v4u*>(to));
-    asm volatile("");  // or the compiler makes one plain store of both
-    if (!past) *static_cast<v4u*>(to) = v;
-}
-
 // First row and number of rows of expert e, from its bounds (b1 is not used
 // in the padded layout); false if they break the rules.
 __device__ inline bool expert_rows(const RowsArg& r, int e, int b0, int b1, int* first, int* count) {

@@ -263,6 +263,22 @@ def test_swiglu_padded(padded):
     assert (h[~p.live] == 7.0).all() and p.status() == 0
 
 
+def test_swiglu_past_the_caches():
+    """Rows and results of more than 256 MiB."""
+    R, inner = 11011, 4096
+    assert R * inner * 6 > 256 << 20
+    g = torch.Generator(device="cuda").manual_seed(15)
+    gu = torch.randn(R, 2 * inner, generator=g, device="cuda").to(torch.bfloat16)
+    h = torch.full((R, inner), 7.0, dtype=torch.bfloat16, device="cuda")
+    bounds = torch.tensor([0, 4000, 4000, R - 3], dtype=torch.int32).cuda()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    M.ep_swiglu(M.moedisp_rows.contiguous(3, R), inner, gu, bounds, h, ws)
+    assert M.ep_check_status(ws) == 0 and (h[R - 3:] == 7.0).all()
+    for lo in range(0, R - 3, 2000):
+        want = swiglu64(gu[lo:min(lo + 2000, R - 3)])
+        within(h[lo:lo + want.shape[0]], want, (2.0 ** -8 + 8 * U) * want.abs() + 2.0 ** -110)
+
+
 def test_swiglu_extremes():
     inf, nan = float("inf"), float("nan")
     g = torch.tensor([inf, -inf, nan, 1.0, 200.0, -200.0, 0.0, -0.0])
