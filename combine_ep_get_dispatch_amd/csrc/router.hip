@@ -28,10 +28,10 @@
 //     softmax               dz = p ([chosen] g - sum_i g_i p_i), all experts
 //     sigmoid               dz = g s (1 - s)
 //
-// What bounds it.  131072 rows of 256 bf16 logits, top-8: 37 us forward (75 MB,
-// 2 TB/s), instructions: about a third each for the sort, the k rounds, and the
-// exponentials with the keys; 31 us backward (142 MB, 4.6 TB/s).  128 rows
-// with bias and groups: 6.7 us, latency of dependent lane exchanges (13 with 16
+// What bounds it.  131072 rows of 256 bf16 logits, top-8: 33 us forward (75 MB,
+// 2.3 TB/s), instructions: about a third each for the sort, the k rounds, and the
+// exponentials with the keys; 29 us backward (142 MB, 5 TB/s).  128 rows
+// with bias and groups: 6.5 us, latency of dependent lane exchanges (13 with 16
 // lanes a row).  The compiler's accesses by index for lists that move up took
 // 343 us forward, binary64 keys for bf16 logits 44.
 #include <type_traits>
@@ -163,33 +163,35 @@ struct Key64 {
 };
 // The bits of a bf16 logit, turned so that they order as integers, above the index.
 struct Key32 {
-    using type = uint32_t;
-    static constexpr uint32_t kNone = 0;  // -inf is 0x7F above the index
-    static __device__ inline uint32_t make(float z, int e) {
-        const uint32_t b = __float_as_uint(z + 0.0f) >> 16;  // -0 becomes 0
-        return (b ^ (b & 0x8000u ? 0xFFFFu : 0x8000u)) << 12 | (uint32_t)(4095 - e);
+    using type = int32_t;
+    static constexpr int32_t kNone = (int32_t)0xF807FFFF;  // the largest key of -inf
+    static __device__ inline int32_t make(float z, int e) {
+        const int32_t b = __float_as_int(z + 0.0f);  // -0 becomes 0
+        return (((b ^ ((b >> 31) & 0x7FFFFFFF)) >> 4) & ~4095) | (4095 - e);
     }
-    static __device__ inline int index(uint32_t key) { return 4095 - (int)(key & 4095u); }
-    static __device__ inline uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
-    static __device__ inline uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
+    static __device__ inline int index(int32_t key) { return 4095 - (key & 4095); }
+    static __device__ inline int32_t larger(int32_t a, int32_t b) { return max(a, b); }
+    static __device__ inline int32_t smaller(int32_t a, int32_t b) { return min(a, b); }
     template <int L>
-    static __device__ inline uint32_t largest(uint32_t v) {
-        auto moved = [](uint32_t x, auto ctrl) {
-            return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xF, 0xF, true);
+    static __device__ inline int32_t largest(int32_t v) {
+        auto moved = [](int32_t x, auto ctrl) {
+            return __builtin_amdgcn_update_dpp(0, x, decltype(ctrl)::value, 0xF, 0xF, true);
         };
         v = max(v, moved(v, std::integral_constant<int, 0xB1>{}));
         v = max(v, moved(v, std::integral_constant<int, 0x4E>{}));
         v = max(v, moved(v, std::integral_constant<int, 0x141>{}));
         v = max(v, moved(v, std::integral_constant<int, 0x140>{}));
         if (L > 16) {
-            auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-            v = max((uint32_t)r[0], (uint32_t)r[1]);
-            r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-            v = max((uint32_t)r[0], (uint32_t)r[1]);
+            auto r = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+            v = max((int32_t)r[0], (int32_t)r[1]);
+            r = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+            v = max((int32_t)r[0], (int32_t)r[1]);
         }
         return v;
     }
-    static __device__ inline uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
+    static __device__ inline int32_t pick(uint32_t mask, int32_t a, int32_t b) {
+        return (int32_t)(((uint32_t)a & mask) | ((uint32_t)b & ~mask));
+    }
 };
 
 // Descending, by Batcher's odd-even merge network.
@@ -216,13 +218,19 @@ __device__ inline float raw_logit(const void* logits, size_t at) {
                 : reinterpret_cast<const float*>(logits)[at];
 }
 // +inf counts as the largest finite number, so that differences are numbers;
-// NaN as -inf, which takes no part.
-__device__ inline float tame(float v) { return v == v ? fminf(v, 0x1.fffffep+127f) : -INFINITY; }
+// NaN as -inf, which takes no part (the larger of NaN and a number is the number).
+__device__ inline float tame(float v) { return fminf(fmaxf(v, -INFINITY), 0x1.fffffep+127f); }
 
 // Lane l's logits of a row: experts (c * L + l) * V .. + V - 1 of chunk c, V
 // at a time; -inf past the last expert.
 template <int P>
 constexpr int piece() { return P < 8 ? P : 8; }
+template <int L, int P>
+__device__ inline int expert_of(int l, int i) {
+    constexpr int V = piece<P>();
+    return (i / V * L + l) * V + i % V;
+}
+
 template <int L, int P, bool BF16>
 __device__ inline void load_row(const RouterArgs& a, size_t row, int l, float z[P]) {
     constexpr int V = piece<P>();
@@ -261,15 +269,12 @@ __device__ inline void load_row(const RouterArgs& a, size_t row, int l, float z[
             for (int i = 0; i < V; ++i) z[c * V + i] = raw_logit<BF16>(a.logits, row * a.E + min(e0 + i, a.E - 1));
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            z[c * V + i] = e0 + i < a.E ? tame(z[c * V + i]) : -INFINITY;
+        for (int i = 0; i < V; ++i) z[c * V + i] = tame(z[c * V + i]);
     }
-}
-
-template <int L, int P>
-__device__ inline int expert_of(int l, int i) {
-    constexpr int V = piece<P>();
-    return (i / V * L + l) * V + i % V;
+    if (a.E == L * P) return;  // no compare per expert (with signed keys: 37 us forward -> 33)
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (expert_of<L, P>(l, i) >= a.E) z[i] = -INFINITY;
 }
 
 // Scores over the chosen ones' common factor, and what divides them.  m is the
@@ -424,8 +429,7 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router(RouterArgs a) {
         if (a.groups > 1) keep_groups<L, P>(a, l, s_keys + (size_t)(threadIdx.x / L) * a.E, key);
     } else {
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-            key[i] = z[i] > -INFINITY ? Key32::make(z[i], expert_of<L, P>(l, i)) : Key32::kNone;
+        for (int i = 0; i < P; ++i) key[i] = Key32::make(z[i], expert_of<L, P>(l, i));
     }
 
     sort_keys<K, P>(key);
@@ -633,8 +637,9 @@ hipError_t launch(const RouterArgs& a, bool backward, hipStream_t stream) {
 }  // namespace
 
 // 16 lanes a row let a wave work on four; a whole wave is quicker where there
-// are few rows (256 experts, 128 rows with bias and groups: 8.7 us a call and 13;
-// 131072 rows: 126 us both directions and 69).
+// are few rows (256 experts with bias and groups, 1024 rows: 12.5 us a call and
+// 6.5; 4096: 12.9 and 10.9; 8192: 16.2 and 18.4.  131072 rows of bf16, both
+// directions: 66 and 121).
 RouterShape router_shape(int T, int E) {
     if (E <= 64) return {16, 4};
     if (E <= 128) return {16, 8};

@@ -157,6 +157,37 @@ def test_rows_without_experts(score, dt):
     assert (w[5, 2:] == 0).all() and abs(float(w[5].sum()) - 1) < 4 * U * 2
 
 
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("E", [64, 256, 255])
+def test_every_kind_of_nan(E, score, dt):
+    """Quiet and signalling NaN of both signs, the type's lowest and highest
+    values and both zeros: NaN is never chosen, the rest keep their order."""
+    z = logits(16, E, dt, 9)
+    if dt == torch.bfloat16:
+        bits, as_int = [0x7FC0, 0xFFC0, 0x7F81, 0xFF81, 0x7FBF, 0xFFFF], torch.int16
+    else:
+        bits, as_int = [0x7FC00000, 0xFFC00000, 0x7F800001, 0xFF800001, 0x7FBFFFFF, 0xFFFFFFFF], torch.int32
+    wide = 1 << (15 if dt == torch.bfloat16 else 31)
+    bits = [b - 2 * wide if b >= wide else b for b in bits]
+    for i, b in enumerate(bits):
+        z.view(as_int)[i, i::3] = b           # among numbers
+        z.view(as_int)[6 + i, 1:] = b         # one number left, the first
+    z[12, :] = torch.finfo(dt).min
+    z[13, :] = -torch.inf
+    z[13, E - 1] = torch.finfo(dt).min
+    z[14, ::2], z[14, 1::2] = 0.0, -0.0
+    z[15, 0] = -torch.inf
+    idx, w = choose(z, 8, score)
+    want_idx, want = router64(z, 8, score)
+    assert torch.equal(idx.long(), want_idx)
+    assert torch.isfinite(w).all()
+    within(w, want, 64 * U * want + 2.0 ** -120)
+    assert (idx[6:12, 1:] == -1).all() and (idx[6:12, 0] == 0).all()
+    assert idx[12].tolist() == idx[14].tolist() == list(range(8))
+    assert idx[13].tolist() == [E - 1] + [-1] * 7
+
+
 def test_bias_masks_and_forces():
     z = logits(64, 32, torch.float32, 5)
     bias = torch.zeros(32)
