@@ -2,7 +2,7 @@
 //
 // Choice.  An expert's choice value c is its logit, or its score plus bias
 // where a bias or groups take part; a row's k largest are chosen, the lowest
-// index first among equals.  A bf16 logit and the index make one integer of 28
+// index first among equals.  A bf16 logit and the index make one integer of 32
 // bits.  Other choice values are kept as a binary64 number whose 12 lowest
 // bits hold the index (turned round for c >= 0, so that a lower index is
 // larger): comparing two keys compares values, then indexes, in one
@@ -161,13 +161,16 @@ struct Key64 {
         return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
     }
 };
-// The bits of a bf16 logit, turned so that they order as integers, above the index.
+// The bits of a bf16 logit, turned so that they order as integers, with the index
+// in the lowest 12.  The 4 above those are zeros, or ones where the bits are
+// turned, but for the largest binary32 number: that stands for +inf and has
+// to be above the largest bf16 one, which they tell it from.
 struct Key32 {
     using type = int32_t;
-    static constexpr int32_t kNone = (int32_t)0xF807FFFF;  // the largest key of -inf
+    static constexpr int32_t kNone = (int32_t)0x807FFFFF;  // the largest key of -inf
     static __device__ inline int32_t make(float z, int e) {
         const int32_t b = __float_as_int(z + 0.0f);  // -0 becomes 0
-        return (((b ^ ((b >> 31) & 0x7FFFFFFF)) >> 4) & ~4095) | (4095 - e);
+        return ((b ^ ((b >> 31) & 0x7FFFFFFF)) & ~4095) | (4095 - e);
     }
     static __device__ inline int index(int32_t key) { return 4095 - (key & 4095); }
     static __device__ inline int32_t larger(int32_t a, int32_t b) { return max(a, b); }
