@@ -47,7 +47,7 @@ __device__ inline bool row_used(const RowsArg& r, int row) {
 // v_rcp_f32 with one correction.  The rows' memory traffic leaves room for
 // about 30 instructions per value: expf and a division are 27 of their own.
 // Beyond +-87, where 2^h would leave the normal range, s is 0 or 1 (for NaN
-// any: its factor v is NaN).
+// any: its factor v is NaN); bf16 results below take gated_below.
 __device__ inline float sigmoid(float v) {
     const float x = __builtin_amdgcn_fmed3f(v, -87.0f, 87.0f);
     const float h = x * -0x1.715476p+0f;
@@ -58,6 +58,21 @@ __device__ inline float sigmoid(float v) {
     const float r = __builtin_amdgcn_rcpf(d);
     const float s = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
     return v < -87.0f ? 0.0f : s;
+}
+
+// g * s * u for a finite g < -87, where s = exp(g) (but for a part of 2^-125) and
+// may lie below binary32's normal range while the product does not: exp(g) =
+// 2^n 2^f (1 + l ln 2), n + f + l = g / ln 2, and 2^n comes last.  2^-20 of u keeps
+// the product before it in range; where that is inexact, the result is zero.
+__device__ inline float gated_below(float g, float u) {
+    const float x = fmaxf(g, -1000.0f);
+    const float h = x * 0x1.715476p+0f;
+    float l = __builtin_fmaf(x, 0x1.715476p+0f, -h);
+    l = __builtin_fmaf(x, 0x1.4ae0c0p-26f, l);
+    const float n = __builtin_rintf(h);
+    const float p = __builtin_amdgcn_exp2f(h - n);
+    const float e = __builtin_fmaf(p, l * 0x1.62e430p-1f, p);
+    return __builtin_ldexpf(x * e * (u * 0x1p-20f), (int)n + 20);
 }
 
 __device__ inline void unpack8(v4u v, float f[8]) {
@@ -158,6 +173,16 @@ __global__ __launch_bounds__(kSwigluThreads, BACKWARD ? 7 : 8) void moedisp_swig
             if (!BACKWARD) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = g[i] * sigmoid(g[i]) * u[i];
+                if constexpr (FMT < 0) {  // (codes are zero there)
+                    float least = g[0];
+#pragma unroll
+                    for (int i = 1; i < 8; ++i) least = fminf(least, g[i]);
+                    if (least < -87.0f) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (g[i] < -87.0f && g[i] > -INFINITY) o[i] = gated_below(g[i], u[i]);
+                    }
+                }
                 v4u* const h = reinterpret_cast<v4u*>(a.h + (size_t)row * a.inner + c);
                 if constexpr (FMT == kBf16)
                     *h = pack8(o);

@@ -459,7 +459,8 @@ int ep_swiglu_quant(const moedisp_rows* rows, int32_t inner, int32_t scale_fmt, 
                     const int32_t* row_bounds, void* h, void* h_scales, void* ws, size_t ws_bytes, void* stream);
 
 /* Gradient of gu, the quantisation taken as the identity:
- *   s = 1 / (1 + exp(-g));  dg = dh*u*s*(1 + g*(1-s));  du = dh*g*s
+ *   s = 1 / (1 + exp(-g)) (zero for finite g < -87);
+ *   dg = dh*u*s*(1 + g*(1-s));  du = dh*g*s
  *   dh            bf16 [max_rows][inner]
  *   dgu           bf16 [max_rows][2*inner] (dg, du) or NULL
  *   dgu_q, dgu_scales  the same gradient before rounding to bf16, quantised
@@ -472,7 +473,8 @@ int ep_swiglu_backward(const moedisp_rows* rows, int32_t inner, int32_t scale_fm
                        size_t ws_bytes, void* stream);
 
 /* ep_swiglu_quant without the quantisation: h bf16 [max_rows][inner], rounded
- * once.  An infinite g gives an infinite product or NaN, as the formula does
+ * once, also for g < -87, where u may be large enough that h is not zero.  An
+ * infinite g gives an infinite product or NaN, as the formula does
  * (an infinite negative g times 0 is NaN). */
 int ep_swiglu(const moedisp_rows* rows, int32_t inner, const void* gu, const int32_t* row_bounds, void* h, void* ws,
               size_t ws_bytes, void* stream);
