@@ -93,13 +93,14 @@ PyObject* checks_arg(PyObject* o, PyObject* const* a, Py_ssize_t nargs, PyObject
             return nullptr;
         }
     }
-    const long long need = PyLong_AsLongLong(a[3]);
+    int overflow;  // sizes of absurd shapes pass 64 bits; no tensor holds that many bytes
+    const long long need = PyLong_AsLongLongAndOverflow(a[3], &overflow);
     if (need == -1 && PyErr_Occurred()) return nullptr;
     PyObject* t = a[1];
     bool good = false;
     if (THPVariable_CheckExact(t)) {
         const at::Tensor& v = THPVariable_Unpack(t);
-        good = v.layout() == at::kStrided && v.is_contiguous() && (long long)v.nbytes() >= need &&
+        good = overflow <= 0 && v.layout() == at::kStrided && v.is_contiguous() && (long long)v.nbytes() >= need &&
                has_type(a[2], reinterpret_cast<PyObject*>(torch::getTHPDtype(v.scalar_type())));
     }
     if (!good) {  // a subclass or none, or something to complain of

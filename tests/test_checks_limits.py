@@ -1,0 +1,41 @@
+"""The binding's argument checks where they meet what is absurd: sizes past 64
+bits.  In C++ and in Python alike (no GPU needed)."""
+import pytest
+import torch
+
+import combine_ep_get_dispatch_amd as M
+from combine_ep_get_dispatch_amd import binding as B
+from test_checks import BOTH, x
+
+
+@pytest.mark.parametrize("cls", BOTH)
+def test_sizes_past_64_bits(cls):
+    A = cls("some_call")
+    with pytest.raises(M.MoeDispError, match=f"needs {2 ** 63}"):
+        A.arg("x", x, B._ROWS_BF16, 2 ** 63)
+    with pytest.raises(M.MoeDispError, match="x is required"):
+        A.arg("x", None, B._ROWS_BF16, 2 ** 80)
+    assert A.arg("x", x, B._ROWS_BF16, -2 ** 80) == x.data_ptr()
+
+
+def test_calls_of_absurd_shapes():
+    rows = M.moedisp_rows.contiguous(2 ** 31 - 1, 4)
+    bounds, ws = torch.zeros(5, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    w = torch.zeros(8, 8)
+    rows_bf16 = torch.zeros(8, dtype=torch.bfloat16)
+    huge = 2 ** 31 - 1
+    router = M.moedisp_router.make(huge, huge, huge)
+    for call in (lambda: M.ep_expert_wgrad_bf16(rows, huge, huge, rows_bf16, rows_bf16, bounds, w, M.FP32, False, ws),
+                 lambda: M.ep_expert_gemm_bf16(rows, huge, huge, 0, rows_bf16, rows_bf16, bounds, w, M.FP32, ws),
+                 lambda: M.ep_expert_gemm_w4(rows, huge, huge, 0, rows_bf16, ws, ws, bounds, w, M.FP32, ws),
+                 lambda: M.ep_router_topk(router, w, None, None, bounds, w)):
+        with pytest.raises(M.MoeDispError):
+            call()
+
+
+@pytest.mark.parametrize("cls", BOTH)
+def test_size_of_a_weight_gradient(cls):
+    """E * N * K * 4 with each at its type's largest is past 2^63."""
+    A = cls("ep_expert_wgrad_bf16")
+    with pytest.raises(M.MoeDispError, match="dw holds"):
+        A.arg("dw", torch.zeros(8, 8), B._F32, (2 ** 31 - 1) ** 3 * 4, written=True)
