@@ -427,6 +427,14 @@ class _Args(_Checks):
         return dev, stream.cuda_stream
 
 
+def _int32(A: _Args, bits: int):
+    """`bits`: the int32 arguments of a call, or-ed together.  ctypes would cut
+    off what does not fit, so that the sizes checked here and those of the call
+    differed.  (A negative argument may hide a large one; the call refuses it.)"""
+    if bits >> 31 not in (0, -1):
+        A.fail("an integer argument does not fit in 32 bits")
+
+
 def _dims(shape: moedisp_shape):
     """(T, H, E, G, k, row bytes, fp32 scales per row) of a shape."""
     T, H, E, G, k = shape.num_tokens, shape.hidden, shape.num_experts, shape.num_groups, shape.topk
@@ -568,6 +576,7 @@ def ep_dispatch_scatter(shape, x, x_scales, topk_idx, topk_weights, tokens_per_e
 
 def _need_quant(A, shape, quant_block, scale_fmt, x, topk_idx, topk_weights, tokens_per_expert, recv_x,
                 recv_scales, recv_src_idx, recv_weights, expert_offsets, slot_to_row, ws):
+    _int32(A, int(quant_block) | int(scale_fmt))
     T, H, E, G, k, rb, nsc = _dims(shape)
     cap = T * k
     blocks = H // int(quant_block) if int(quant_block) > 0 else 0
@@ -632,6 +641,7 @@ def ep_layout_dispatch_small_padded(shape, expert_capacity, expert_stride, row_b
                                     topk_weights, tokens_per_expert, tokens_per_group, is_token_in_group, recv_x,
                                     recv_scales, recv_src_idx, recv_weights, slot_to_row, ws, stream=None):
     A = _Args("ep_layout_dispatch_small_padded")
+    _int32(A, int(expert_capacity) | int(expert_stride) | int(row_base))
     T, H, E, G, k, rb, nsc = _dims(shape)
     rows = E * max(int(expert_stride), 0)
     A.need("x", x, _rows_dtypes(shape), T * rb)
@@ -712,6 +722,7 @@ def _out_bytes(rows: int, H: int, out_dtype: int) -> int:
 def ep_group_reduce(shape, expert_out, recv_src_idx, recv_weights, slot_to_row, group_offsets, group_out, out_dtype,
                     ws, stream=None):
     A = _Args("ep_group_reduce")
+    _int32(A, int(out_dtype))
     T, H, E, G, k, rb, nsc = _dims(shape)
     gr = T * min(G, k)
     A.need("expert_out", expert_out, _ROWS_BF16, T * k * H * 2)
@@ -729,6 +740,7 @@ def ep_group_reduce(shape, expert_out, recv_src_idx, recv_weights, slot_to_row, 
 
 def ep_combine_groups(shape, group_rows, recv_src_idx, token_group_row, out, out_dtype, ws, stream=None):
     A = _Args("ep_combine_groups")
+    _int32(A, int(out_dtype))
     T, H, E, G, k, rb, nsc = _dims(shape)
     gr = T * min(G, k)
     A.need("group_rows", group_rows, _ROWS_BF16, gr * H * 2)
@@ -744,6 +756,7 @@ def ep_combine_groups(shape, group_rows, recv_src_idx, token_group_row, out, out
 
 def ep_combine(shape, expert_out, recv_src_idx, recv_weights, slot_to_row, out, out_dtype, ws, stream=None):
     A = _Args("ep_combine")
+    _int32(A, int(out_dtype))
     T, H, E, G, k, rb, nsc = _dims(shape)
     A.need("expert_out", expert_out, _ROWS_BF16, T * k * H * 2)
     A.need("recv_src_idx", recv_src_idx, _INT32, 4 * T * k, optional=True)
@@ -760,6 +773,7 @@ def ep_combine(shape, expert_out, recv_src_idx, recv_weights, slot_to_row, out, 
 def ep_combine_padded(shape, expert_stride, expert_out, recv_src_idx, recv_weights, slot_to_row, out, out_dtype, ws,
                       stream=None):
     A = _Args("ep_combine_padded")
+    _int32(A, int(expert_stride) | int(out_dtype))
     T, H, E, G, k, rb, nsc = _dims(shape)
     rows = E * max(int(expert_stride), 0)
     A.need("expert_out", expert_out, _ROWS_BF16, rows * H * 2)
@@ -807,6 +821,7 @@ def _on(dev: int, call: str, *args):
 def ep_expert_gemm(rows, n, k, scale_fmt, x, x_scales, w, w_scales, row_bounds, y, out_dtype, ws, stream=None):
     A = _Args("ep_expert_gemm")
     n, k, scale_fmt, out_dtype = int(n), int(k), int(scale_fmt), int(out_dtype)
+    _int32(A, n | k | scale_fmt | out_dtype)
     R, E, bounds = _rows_of(A, rows, row_bounds)
     N, K = max(n, 0), max(k, 0)
     kb = K // 128
@@ -822,6 +837,7 @@ def ep_expert_gemm(rows, n, k, scale_fmt, x, x_scales, w, w_scales, row_bounds, 
 def ep_expert_wgrad(rows, n, k, scale_fmt, x, x_scales, dy, row_bounds, dw, out_dtype, accumulate, ws, stream=None):
     A = _Args("ep_expert_wgrad")
     n, k, scale_fmt, out_dtype = int(n), int(k), int(scale_fmt), int(out_dtype)
+    _int32(A, n | k | scale_fmt | out_dtype)
     R, E, bounds = _rows_of(A, rows, row_bounds)
     N, K = max(n, 0), max(k, 0)
     args = (A.arg("x", x, _ROWS_FP8, R * K), _scales(A, "x_scales", x_scales, scale_fmt, R * (K // 128)),
@@ -835,6 +851,7 @@ def ep_expert_wgrad(rows, n, k, scale_fmt, x, x_scales, dy, row_bounds, dw, out_
 def ep_swiglu_quant(rows, inner, scale_fmt, gu, row_bounds, h, h_scales, ws, stream=None):
     A = _Args("ep_swiglu_quant")
     inner, scale_fmt = int(inner), int(scale_fmt)
+    _int32(A, inner | scale_fmt)
     R, _, bounds = _rows_of(A, rows, row_bounds)
     I = max(inner, 0)
     args = (A.arg("gu", gu, _ROWS_BF16, R * I * 4), bounds, A.arg("h", h, _ROWS_FP8, R * I, written=True),
@@ -847,6 +864,7 @@ def ep_swiglu_quant(rows, inner, scale_fmt, gu, row_bounds, h, h_scales, ws, str
 def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, dgu_scales, ws, stream=None):
     A = _Args("ep_swiglu_backward")
     inner, scale_fmt = int(inner), int(scale_fmt)
+    _int32(A, inner | scale_fmt)
     R, _, bounds = _rows_of(A, rows, row_bounds)
     I = max(inner, 0)
     args = (A.arg("gu", gu, _ROWS_BF16, R * I * 4), A.arg("dh", dh, _ROWS_BF16, R * I * 2), bounds,
@@ -861,6 +879,7 @@ def ep_swiglu_backward(rows, inner, scale_fmt, gu, dh, row_bounds, dgu, dgu_q, d
 def ep_swiglu(rows, inner, gu, row_bounds, h, ws, stream=None):
     A = _Args("ep_swiglu")
     inner = int(inner)
+    _int32(A, inner)
     R, _, bounds = _rows_of(A, rows, row_bounds)
     I = max(inner, 0)
     args = (A.arg("gu", gu, _ROWS_BF16, R * I * 4), bounds, A.arg("h", h, _ROWS_BF16, R * I * 2, written=True))
@@ -872,6 +891,7 @@ def ep_swiglu(rows, inner, gu, row_bounds, h, ws, stream=None):
 def ep_expert_gemm_bf16(rows, n, k, w_layout, x, w, row_bounds, y, out_dtype, ws, stream=None):
     A = _Args("ep_expert_gemm_bf16")
     n, k, w_layout, out_dtype = int(n), int(k), int(w_layout), int(out_dtype)
+    _int32(A, n | k | w_layout | out_dtype)
     R, E, bounds = _rows_of(A, rows, row_bounds)
     N, K = max(n, 0), max(k, 0)
     args = (A.arg("x", x, _ROWS_BF16, R * K * 2), A.arg("w", w, _ROWS_BF16, E * N * K * 2), bounds,
@@ -884,6 +904,7 @@ def ep_expert_gemm_bf16(rows, n, k, w_layout, x, w, row_bounds, y, out_dtype, ws
 def ep_expert_wgrad_bf16(rows, n, k, x, dy, row_bounds, dw, out_dtype, accumulate, ws, stream=None):
     A = _Args("ep_expert_wgrad_bf16")
     n, k, out_dtype = int(n), int(k), int(out_dtype)
+    _int32(A, n | k | out_dtype)
     R, E, bounds = _rows_of(A, rows, row_bounds)
     N, K = max(n, 0), max(k, 0)
     args = (A.arg("x", x, _ROWS_BF16, R * K * 2), A.arg("dy", dy, _ROWS_BF16, R * N * 2), bounds,
@@ -896,6 +917,7 @@ def ep_expert_wgrad_bf16(rows, n, k, x, dy, row_bounds, dw, out_dtype, accumulat
 def ep_expert_gemm_w4(rows, n, k, w4_fmt, x, w, w_scales, row_bounds, y, out_dtype, ws, stream=None):
     A = _Args("ep_expert_gemm_w4")
     n, k, w4_fmt, out_dtype = int(n), int(k), int(w4_fmt), int(out_dtype)
+    _int32(A, n | k | w4_fmt | out_dtype)
     R, E, bounds = _rows_of(A, rows, row_bounds)
     N, K = max(n, 0), max(k, 0)
     sdt, sbytes = (_ROWS_BF16, E * (K // 128) * N * 2) if w4_fmt == W4_INT4 else (_U8, E * (K // 32) * N)

@@ -39,3 +39,34 @@ def test_size_of_a_weight_gradient(cls):
     A = cls("ep_expert_wgrad_bf16")
     with pytest.raises(M.MoeDispError, match="dw holds"):
         A.arg("dw", torch.zeros(8, 8), B._F32, (2 ** 31 - 1) ** 3 * 4, written=True)
+
+
+def test_integers_past_32_bits():
+    """ctypes would cut them off: FP32 + 2^32 would be checked as bf16 results
+    and written as binary32, and 256 - 2^32 channels need no memory here."""
+    past, cut = 2 ** 32, -2 ** 32
+    r = M.moedisp_rows.contiguous(1, 4)
+    t = torch.zeros(0)
+    for call in (lambda v: M.ep_expert_gemm(r, 256, 256, 0, t, t, t, t, t, t, M.FP32 + v, t),
+                 lambda v: M.ep_expert_gemm(r, 256, 256 + v, 0, t, t, t, t, t, t, M.FP32, t),
+                 lambda v: M.ep_expert_wgrad(r, 256 + v, 256, 0, t, t, t, t, t, M.FP32, False, t),
+                 lambda v: M.ep_swiglu_quant(r, 256 + v, 0, t, t, t, t, t),
+                 lambda v: M.ep_swiglu_backward(r, 256, v, t, t, t, t, t, t, t),
+                 lambda v: M.ep_swiglu(r, 256 + v, t, t, t, t),
+                 lambda v: M.ep_expert_gemm_bf16(r, 256, 256, 1 + v, t, t, t, t, M.FP32, t),
+                 lambda v: M.ep_expert_gemm_bf16(r, 256, 256, 1, t, t, t, t, M.FP32 + v, t),
+                 lambda v: M.ep_expert_wgrad_bf16(r, 256, 256 + v, t, t, t, t, M.FP32, False, t),
+                 lambda v: M.ep_expert_gemm_w4(r, 256, 256, M.W4_INT4 + v, t, t, t, t, t, M.FP32, t)):
+        for v in (past, cut):
+            with pytest.raises(M.MoeDispError, match="32 bits"):
+                call(v)
+    shape = M.moedisp_shape.make(4, 256, 4, 2, 2)
+    for call in (lambda v: M.ep_combine(shape, t, t, t, t, t, M.FP32 + v, t),
+                 lambda v: M.ep_combine_padded(shape, 4 + v, t, t, t, t, t, M.FP32, t),
+                 lambda v: M.ep_combine_groups(shape, t, t, t, t, M.FP32 + v, t),
+                 lambda v: M.ep_group_reduce(shape, t, t, t, t, t, t, M.FP32 + v, t),
+                 lambda v: M.ep_dispatch_quant(shape, 128, 1 + v, *[t] * 11),
+                 lambda v: M.ep_layout_dispatch_small_padded(shape, 4, 4 + v, 0, *[t] * 13)):
+        for v in (past, cut):
+            with pytest.raises(M.MoeDispError, match="32 bits"):
+                call(v)
