@@ -1034,9 +1034,15 @@ def ep_router_plan_query(router) -> dict:
     return _as_dict(info)
 
 
+def _probe_bytes(A, name, t, nbytes):
+    if int(nbytes) < 0:
+        A.fail("nbytes is negative")  # size_t would take it as a large one
+    A.need(name, t, _BYTES, int(nbytes))
+
+
 def ep_probe_read(src, nbytes: int, sink, stream=None):
     A = _Args("ep_probe_read")
-    A.need("src", src, _BYTES, int(nbytes))
+    _probe_bytes(A, "src", src, nbytes)
     A.need("sink", sink, _BYTES, 16)
     A.done()
     _check(A.call, load().ep_probe_read(_p(src), int(nbytes), _p(sink), _s(stream)))
@@ -1044,15 +1050,15 @@ def ep_probe_read(src, nbytes: int, sink, stream=None):
 
 def ep_probe_copy(dst, src, nbytes: int, stream=None):
     A = _Args("ep_probe_copy")
-    A.need("dst", dst, _BYTES, int(nbytes))
-    A.need("src", src, _BYTES, int(nbytes))
+    _probe_bytes(A, "dst", dst, nbytes)
+    _probe_bytes(A, "src", src, nbytes)
     A.done()
     _check(A.call, load().ep_probe_copy(_p(dst), _p(src), int(nbytes), _s(stream)))
 
 
 def ep_probe_fill(dst, nbytes: int, shuffled: bool = False, stream=None):
     A = _Args("ep_probe_fill")
-    A.need("dst", dst, _BYTES, int(nbytes))
+    _probe_bytes(A, "dst", dst, nbytes)
     A.done()
     _check(A.call, load().ep_probe_fill(_p(dst), int(nbytes), 1 if shuffled else 0, _s(stream)))
 

@@ -70,3 +70,10 @@ def test_integers_past_32_bits():
         for v in (past, cut):
             with pytest.raises(M.MoeDispError, match="32 bits"):
                 call(v)
+
+
+def test_probes_of_negative_sizes():
+    t = torch.zeros(64)
+    for call in (lambda: M.ep_probe_read(t, -16, t), lambda: M.ep_probe_copy(t, t, -16), lambda: M.ep_probe_fill(t, -4096)):
+        with pytest.raises(M.MoeDispError, match="negative"):
+            call()
