@@ -365,7 +365,7 @@ try:
     from . import _checks
     _checks.use_stream_of(_raw_stream)
     _Checks = _checks.Checks
-except ImportError:  # not built, or for another torch
+except ImportError:  # not built, or for another torch or Python (it looks itself)
     _Checks = _PyChecks
 
 

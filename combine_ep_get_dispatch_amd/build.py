@@ -50,7 +50,8 @@ def build_checks(out: str = CHECKS, verbose: bool = False) -> str:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = out + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *inc, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DMOEDISP_BUILT_FOR="{torch.version.__version__} {torch.version.git_version}"', *inc, "-o", tmp,
            os.path.join(CSRC, "checks.cpp"), f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
            f"-Wl,-rpath,{lib}"]
     if verbose:

@@ -2,6 +2,10 @@
 // Python is more than a small call's launch (four tensors: 2.0 us there, 0.3
 // here).  Whatever is not in order is handed to the Python method of the same
 // purpose, which says what is wrong; nothing is refused here alone.
+//
+// Tensors are read by torch's inline accessors, whose offsets are those of the
+// torch that this was built for.  With another one the import fails, and the
+// binding checks in Python.
 #include <Python.h>
 #include <structmember.h>
 #include <torch/csrc/Dtype.h>
@@ -186,9 +190,32 @@ PyMethodDef functions[] = {
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_checks", nullptr, -1, functions, nullptr, nullptr, nullptr, nullptr};
 
+// Whether Python and torch are those of the build (MOEDISP_BUILT_FOR: torch's
+// version and commit).  If not, or on an error, an exception is set.
+bool as_built() {
+    PyObject* hex = PySys_GetObject("hexversion");
+    const unsigned long python = hex ? PyLong_AsUnsignedLong(hex) : 0;
+    if (PyErr_Occurred()) return false;
+    if (python >> 16 != (unsigned long)PY_VERSION_HEX >> 16) {
+        PyErr_SetString(PyExc_ImportError, "_checks was built for another Python");
+        return false;
+    }
+    THPObjectPtr version(PyImport_ImportModule("torch.version"));
+    THPObjectPtr number(version ? PyObject_GetAttrString(version.get(), "__version__") : nullptr);
+    THPObjectPtr commit(number ? PyObject_GetAttrString(version.get(), "git_version") : nullptr);
+    THPObjectPtr both(commit ? PyUnicode_FromFormat("%S %S", number.get(), commit.get()) : nullptr);
+    if (!both) return false;
+    if (PyUnicode_CompareWithASCIIString(both.get(), MOEDISP_BUILT_FOR) != 0) {
+        PyErr_Format(PyExc_ImportError, "_checks was built for torch %s, this is %S", MOEDISP_BUILT_FOR, both.get());
+        return false;
+    }
+    return true;
+}
+
 }  // namespace
 
 PyMODINIT_FUNC PyInit__checks() {
+    if (!as_built()) return nullptr;
     type.tp_name = "combine_ep_get_dispatch_amd._checks.Checks";
     type.tp_basicsize = sizeof(Checks);
     type.tp_flags = Py_TPFLAGS_DEFAULT | Py_TPFLAGS_BASETYPE;
