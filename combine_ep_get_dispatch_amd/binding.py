@@ -9,6 +9,7 @@ no fallback: if libmoedisp.so is missing, every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 import os
 from typing import Optional
 
@@ -333,8 +334,9 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 
 class _PyChecks:
-    """_checks.Checks (csrc/checks.cpp) in Python."""
+    """_checks.Checks (csrc/checks.cpp) in Python, with its errors."""
     __slots__ = ("call", "tensors", "read", "out")
+    MAX_ARGS = 24
 
     def __init__(self, call: str):
         self.call = call
@@ -343,11 +345,16 @@ class _PyChecks:
     def arg(self, name: str, t, dtypes, nbytes: int, optional: bool = False, written: bool = False):
         """As need(); returns the tensor's address (None for none).  The call
         writes to a tensor that is `written`."""
+        nbytes = operator.index(nbytes)
+        if dtypes is not None and type(dtypes) is not tuple:
+            raise TypeError("arg: dtypes must be a tuple or None")
         if type(t) is not torch.Tensor or (dtypes is not None and t.dtype not in dtypes) or not t.is_contiguous() \
                 or t.nbytes < nbytes:
             self.need(name, t, dtypes, nbytes, optional)  # takes a subclass or none, else says what is wrong
             if t is None:
                 return None
+        if len(self.read) + len(self.out) == self.MAX_ARGS:
+            raise TypeError("arg: too many tensors")
         at = t.data_ptr()
         (self.out if written else self.read).append((at, at + t.nbytes, name, t))
         return at

@@ -77,3 +77,21 @@ def test_probes_of_negative_sizes():
     for call in (lambda: M.ep_probe_read(t, -16, t), lambda: M.ep_probe_copy(t, t, -16), lambda: M.ep_probe_fill(t, -4096)):
         with pytest.raises(M.MoeDispError, match="negative"):
             call()
+
+
+@pytest.mark.parametrize("cls", BOTH)
+def test_misuse_raises_alike(cls):
+    """Calls that the binding itself never makes: TypeError in both forms, and
+    no more tensors than a call has."""
+    A = cls("c")
+    for bad in (("x",), ("x", x, None, "many"), ("x", None, None, "many", True), ("x", x, None, 1.5),
+                ("x", x, [torch.bfloat16], 1), ("x", x, torch.bfloat16, 1), ("x", x, None, 1, False, False, 1)):
+        with pytest.raises(TypeError):
+            A.arg(*bad)
+    with pytest.raises(TypeError):
+        A.arg("x", x, None, 1, wrong=True)
+    for _ in range(24):
+        A.arg("x", x, None, 1)
+    A.arg("none", None, None, 1, True)
+    with pytest.raises(TypeError):
+        A.arg("x", x, None, 1)
