@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,8 +43,21 @@ def build(out: str = LIB, extra_flags=(), verbose: bool = False) -> str:
 CHECKS = os.path.join(HERE, "_checks.so")
 
 
-def build_checks(out: str = CHECKS, verbose: bool = False) -> str:
-    """The binding works without it, more slowly."""
+def build_checks(out: str = CHECKS, verbose: bool = False) -> str | None:
+    """The binding works without it, more slowly: where the host compiler or
+    torch's headers are missing this says so, takes away what an earlier build
+    left, and returns None."""
+    try:
+        return _build_checks(out, verbose)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        print(f"{os.path.basename(out)} was not built ({e}): the binding checks its arguments in Python", file=sys.stderr)
+        for left in (out, out + ".tmp"):
+            if os.path.exists(left):
+                os.remove(left)
+        return None
+
+
+def _build_checks(out: str, verbose: bool) -> str:
     import torch
     from torch.utils import cpp_extension
     inc = [f"-I{p}" for p in [sysconfig.get_paths()["include"], *cpp_extension.include_paths()]]
