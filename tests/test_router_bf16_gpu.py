@@ -5,7 +5,7 @@ import torch
 
 import combine_ep_get_dispatch_amd as M
 from bf16_reference import router64
-from test_router_gpu import SCORES, U, choose, logits, within
+from test_router_gpu import SCORES, U, check, choose, logits, within
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,50 @@ def test_infinity_is_above_the_largest_number(T, E, score):
     else:
         expect = torch.full((T, 5), 0.2, device="cuda")
     within(w, expect.double(), 8 * U * expect.double())
+
+
+@pytest.mark.parametrize("normalise", [True, False])
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("T,E", EXPERTS)
+def test_bias(T, E, score, normalise):
+    """Rounded logits, many of which are equal, with a bias."""
+    bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E)).cuda()
+    check(logits(T, E, torch.bfloat16, T + E), 8, score, bias, normalise=normalise, scale=2.5)
+
+
+@pytest.mark.parametrize("biased", [True, False])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("T,E", EXPERTS)
+def test_groups(T, E, score, best, biased):
+    """4 of 8 groups, as for a large model's router, in every shape."""
+    bias = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E)).cuda() if biased else None
+    check(logits(T, E, torch.bfloat16, T + E), 8, score, bias, groups=8 if E % 8 == 0 else 4, topk_groups=4,
+          group_best=best)
+
+
+@pytest.mark.parametrize("T,E,k,G,tg", [(5, 4096, 16, 64, 64), (40, 64, 4, 64, 5), (21, 1024, 32, 32, 4), (11, 39, 3, 3, 1)])
+def test_many_groups(T, E, k, G, tg):
+    bias = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E)).cuda()
+    check(logits(T, E, torch.bfloat16, T + E), k, M.SCORE_SIGMOID, bias, groups=G, topk_groups=tg, normalise=False)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("T,E", EXPERTS)
+def test_masked_and_infinite_logits_with_bias_and_groups(T, E, score):
+    """-inf and NaN take no part; +inf has the score of the largest number."""
+    z = logits(T, E, torch.bfloat16, T + E)
+    z[0, ::2], z[1, 1::2], z[2, E // 2:] = -torch.inf, float("nan"), -torch.inf
+    z[0, 1] = torch.finfo(torch.bfloat16).max
+    bias = 0.2 * torch.randn(E, generator=torch.Generator().manual_seed(E)).cuda()
+    finite = torch.where(torch.isfinite(z), z, -torch.inf)
+    for kw in (dict(), dict(groups=8 if E % 8 == 0 else 4, topk_groups=2)):
+        for b in (None, bias):
+            idx, w = choose(z, 8, score, b, **kw)
+            want_idx, want = router64(finite, 8, score, b, **kw)
+            assert torch.equal(idx.long(), want_idx)
+            within(w, want, 64 * U * want + 2.0 ** -120)
+            top = z.clone()
+            top[0, 1] = torch.inf
+            again, w2 = choose(top, 8, score, b, **kw)
+            assert torch.equal(again, idx) and torch.equal(w2, w)
