@@ -533,9 +533,11 @@ typedef enum {
  *   y          [max_rows][n] bf16 or fp32 (out_dtype).
  * E2M1: a weight times its scale is taken as bf16 number, infinite beyond its
  * range (NaN times an x of 0).  INT4: a group's sums of x times the unsigned
- * codes 0 .. 15, and of 8 x, are binary32, so that x has to stay below 2^116; a
- * row that holds an infinity gives NaN.  Rows, bounds, ws, overlap and alignment
- * as said at moedisp_rows (UE8M0 scales: 4 bytes, bf16 scales: 4 bytes).
+ * codes 0 .. 15, and of 8 x, are binary32, so that x has to stay below 2^116, a
+ * row that holds an infinity gives NaN, and a group's sum is off by up to about
+ * 2^-15 of the sum of (code + 8) |x|, also where the weights are small or zero.
+ * Rows, bounds, ws, overlap and alignment as said at moedisp_rows (UE8M0 scales:
+ * 4 bytes, bf16 scales: 4 bytes).
  * Equal inputs give equal bits.  Status bits: BAD_LAYOUT. */
 int ep_expert_gemm_w4(const moedisp_rows* rows, int32_t n, int32_t k, int32_t w4_fmt, const void* x, const void* w,
                       const void* w_scales, const int32_t* row_bounds, void* y, int32_t out_dtype, void* ws,
