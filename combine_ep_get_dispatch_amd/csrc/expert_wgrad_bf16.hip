@@ -165,8 +165,8 @@ __global__ __launch_bounds__(64 * WN * WK) void moedisp_expert_wgrad_bf16(Expert
                 for (int j = 0; j < T::kNT; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i & 1], b[j], acc[i][j], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
-                // behind the products: step s + 3 into the place of step
-                // s - 1, which all waves have read
+                // behind the products: step s + kStages - 1 into the place of
+                // step s - 1, which all waves have read
                 if (i == 0) load_x(s + kStages - 1, next);
                 if (i == 1) load_dy(s + kStages - 1, next);
                 if (i < 2) __builtin_amdgcn_sched_barrier(0);

@@ -498,7 +498,7 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router_backward(Router
 
     int e[kSlots];
     float zs[kSlots], g[kSlots], m = -INFINITY;
-    bool bad = false, any = false;
+    bool bad = false;
 #pragma unroll
     for (int h = 0; h < kSlots; ++h) {
         const int j = h * L + l;
@@ -508,7 +508,6 @@ __global__ __launch_bounds__(kRouterThreads) void moedisp_router_backward(Router
         if (e[h] >= a.E) e[h] = -1;
         zs[h] = e[h] >= 0 ? tame(raw_logit<BF16>(a.logits, row * a.E + e[h])) : -INFINITY;
         if (!(zs[h] > -INFINITY)) e[h] = -1;  // takes no part
-        any |= e[h] >= 0;
         g[h] = e[h] >= 0 ? a.scale * a.weights[row * a.k + j] : 0.0f;
         m = e[h] >= 0 ? fmaxf(m, zs[h]) : m;
     }

@@ -11,7 +11,7 @@
 // both forms of the gradient (5.0 TB/s).  Workgroups stay resident and take
 // row after row, so that the row bounds are checked once each; one workgroup
 // a row took 98 us, two or four resident a unit 99 and 88.  bf16 results: 403 MB
-// in 73 us (5.5 TB/s).
+// in 72 us (5.6 TB/s).
 #include "experts_common.h"
 
 namespace moedisp {
@@ -241,8 +241,13 @@ hipError_t launch_swiglu(const SwigluArgs& a, int scale_fmt, hipStream_t stream)
     return launch<false>(a, scale_fmt, stream);
 }
 // Where rows and results are more than the memory-side cache holds, they go
-// past the caches: 73 us instead of 80 (32768 rows of 2048, none of them cached;
+// past the caches: 72 us instead of 80 (32768 rows of 2048, none of them cached;
 // called again on the same rows 71 instead of 64 with results alone past them).
+// Between an expert's two products it makes no difference: activation and second
+// product of 32768 rows take 565 us either way (8 experts, 2048 -> 4096), 1687 and
+// 1709 through the caches (256 experts, 2048 -> 7168); nor where few of a padded
+// buffer's rows are used (32 experts, 32 of 1024 rows each: 112 and 113; 256 of
+// 1024: 138 and 145), so that max_rows may decide.
 hipError_t launch_swiglu_bf16(const SwigluArgs& a, hipStream_t stream) {
     const long long blocks = swiglu_blocks(a.r.max_rows, a.blocks, false);
     if ((long long)a.r.max_rows * a.inner * 6 > kCacheBytes)
