@@ -7,7 +7,7 @@
 //
 // What bounds it.  128 rows an expert (256 experts, 7168 -> 4096): the weights
 // from HBM, 15.7 GB in 2.80 ms, 5.6 TB/s (loads alone 2.83 ms, products alone
-// 1.42).  4096 rows (8 experts, 4096 -> 8192): 1.72 ms, 1.28 PFLOP/s; products
+// 1.42).  4096 rows (8 experts, 4096 -> 8192): 1.76 ms, 1.25 PFLOP/s; products
 // alone take 1.29 ms and loads alone 1.23, which do not overlap fully.  KN at 122
 // rows, skewed (256 experts, 7168 -> 2048): 1.74 ms, loads alone 1.68.
 //

@@ -3,7 +3,7 @@
 //
 // Products are exact and sums are binary32; bf16 results are rounded once.
 //
-// What bounds it.  Many rows (32768 over 8 experts, 4096 x 4096): 0.87 ms, 1.26
+// What bounds it.  Many rows (32768 over 8 experts, 4096 x 4096): 0.90 ms, 1.22
 // PFLOP/s, products with the transposing reads beside them (matrix units 0.6 of
 // the time).  Few rows (7782 over 64, 7168 x 2048, fp32): the writes, 3.8 GB in
 // 0.86 ms, 4.4 TB/s (7176 x 1992, tiles cut at both edges: 0.92 ms).  An expert's

@@ -28,9 +28,9 @@
 //     softmax               dz = p ([chosen] g - sum_i g_i p_i), all experts
 //     sigmoid               dz = g s (1 - s)
 //
-// What bounds it.  131072 rows of 256 bf16 logits, top-8: 33 us forward (75 MB,
-// 2.3 TB/s), instructions: about a third each for the sort, the k rounds, and the
-// exponentials with the keys; 29 us backward (142 MB, 5 TB/s).  128 rows
+// What bounds it.  131072 rows of 256 bf16 logits, top-8: 32 us forward (75 MB,
+// 2.4 TB/s), instructions: about a third each for the sort, the k rounds, and the
+// exponentials with the keys; 28 us backward (142 MB, 5 TB/s).  128 rows
 // with bias and groups: 6.5 us, latency of dependent lane exchanges (13 with 16
 // lanes a row).  The compiler's accesses by index for lists that move up took
 // 343 us forward, binary64 keys for bf16 logits 44.
