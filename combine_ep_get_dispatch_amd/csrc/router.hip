@@ -281,7 +281,8 @@ __device__ inline void load_row(const RouterArgs& a, size_t row, int l, float z[
 }
 
 // Scores over the chosen ones' common factor, and what divides them.  m is the
-// largest logit among those that count.
+// largest logit among those that count.  (The difference is rounded: a score far
+// below the largest is off by |z - m| half steps, at most 87.)
 __device__ inline float part(bool sigmoid, float z, float m) {
     if (!sigmoid) return exp32(z - m);
     return exp32(fminf(z, 0.0f) - fminf(m, 0.0f)) / (1.0f + exp32(-fabsf(z)));

@@ -566,7 +566,8 @@ typedef struct {
 /* The choice of k experts for each token, and their weights: what dispatch,
  * combine and the balance loss take as topk_idx and topk_weights.
  *   choice value  the logit where there is neither bias nor groups, else
- *                 score + bias, to the nearest number of 41 bits.
+ *                 score + bias, to the nearest number of 41 bits (a score
+ *                 below exp(-700) is 0 there).
  *   num_groups    above 1: only the topk_groups groups of the largest value
  *                 (to 41 bits) are chosen from.
  * Among equals the lowest index comes first.  The k largest, in descending

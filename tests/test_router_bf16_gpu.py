@@ -85,3 +85,15 @@ def test_masked_and_infinite_logits_with_bias_and_groups(T, E, score):
             top[0, 1] = torch.inf
             again, w2 = choose(top, 8, score, b, **kw)
             assert torch.equal(again, idx) and torch.equal(w2, w)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", SCORES)
+def test_scores_too_small_to_tell_apart(score, dt):
+    """With groups the choice goes by scores, and those below exp(-700) are
+    equal; without, it goes by logits."""
+    z = torch.tensor([[0, -800, -752, -792, -704, -900, -720, -880]]).to(dt).cuda()
+    idx, _ = choose(z, 8, score, groups=2, topk_groups=2)
+    assert idx[0].tolist() == list(range(8))
+    idx, _ = choose(z, 8, score)
+    assert idx[0].tolist() == [0, 4, 6, 2, 3, 1, 7, 5]
