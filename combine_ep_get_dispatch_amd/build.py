@@ -49,7 +49,7 @@ def build_checks(out: str = CHECKS, verbose: bool = False) -> str | None:
     left, and returns None."""
     try:
         return _build_checks(out, verbose)
-    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+    except (ImportError, AttributeError, OSError, subprocess.CalledProcessError) as e:
         print(f"{os.path.basename(out)} was not built ({e}): the binding checks its arguments in Python", file=sys.stderr)
         for left in (out, out + ".tmp"):
             if os.path.exists(left):

@@ -191,11 +191,10 @@ PyMethodDef functions[] = {
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_checks", nullptr, -1, functions, nullptr, nullptr, nullptr, nullptr};
 
 // Whether Python and torch are those of the build (MOEDISP_BUILT_FOR: torch's
-// version and commit).  If not, or on an error, an exception is set.
+// version and commit).  If not, or if that cannot be told, ImportError is set.
 bool as_built() {
     PyObject* hex = PySys_GetObject("hexversion");
     const unsigned long python = hex ? PyLong_AsUnsignedLong(hex) : 0;
-    if (PyErr_Occurred()) return false;
     if (python >> 16 != (unsigned long)PY_VERSION_HEX >> 16) {
         PyErr_SetString(PyExc_ImportError, "_checks was built for another Python");
         return false;
@@ -204,7 +203,10 @@ bool as_built() {
     THPObjectPtr number(version ? PyObject_GetAttrString(version.get(), "__version__") : nullptr);
     THPObjectPtr commit(number ? PyObject_GetAttrString(version.get(), "git_version") : nullptr);
     THPObjectPtr both(commit ? PyUnicode_FromFormat("%S %S", number.get(), commit.get()) : nullptr);
-    if (!both) return false;
+    if (!both) {
+        PyErr_SetString(PyExc_ImportError, "_checks was built for a torch that tells its version and commit");
+        return false;
+    }
     if (PyUnicode_CompareWithASCIIString(both.get(), MOEDISP_BUILT_FOR) != 0) {
         PyErr_Format(PyExc_ImportError, "_checks was built for torch %s, this is %S", MOEDISP_BUILT_FOR, both.get());
         return false;

@@ -33,6 +33,6 @@ def test_as_built():
 
 
 @pytest.mark.parametrize("other", ["torch.version.__version__ = '9.9.9'", "torch.version.git_version = '0' * 40",
-                                   "sys.hexversion = 0x030900F0"])
+                                   "del torch.version.git_version", "sys.hexversion = 0x030900F0"])
 def test_another_version_falls_back(other):
     run("import sys, torch\n" + other + REFUSED)
